@@ -56,7 +56,7 @@ NOMINAL_HBM_GBS = 8000.0
 FALLBACK_HBM_GBS = 6650.0
 L2_BYTES = 126 * 1024 * 1024
 KERNEL_SOURCES = [os.path.join(ROOT, "ffn_gated_activation_b200", "csrc", n)
-                  for n in ("situ_glu.cu", "situ_fused_gemm.cuh")]
+                  for n in ("situ_glu.cu", "situ_device.cuh", "situ_fused_gemm.cuh")]
 TRAFFIC_FILE = os.path.join(ROOT, "profiles", "ncu_traffic.json")
 
 

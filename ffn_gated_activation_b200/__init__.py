@@ -28,6 +28,17 @@ from .functional import (
     situlu,
     weighted_situ,
 )
+from .block import (
+    AddRMSNormFunction,
+    add_rms_norm,
+    situ_glu_moe_fwd,
+    situ_glu_nvfp4_dequantize,
+    situ_glu_nvfp4_gemm,
+    situ_glu_nvfp4_quantize,
+    situ_glu_rms_norm_bwd,
+    situ_glu_rms_norm_fwd,
+    situ_glu_rms_norm_fwd_mxfp8,
+)
 
 __all__ = [
     "abi",
@@ -50,4 +61,13 @@ __all__ = [
     "situ_glu_fc2_dgrad_bwd",
     "situlu",
     "weighted_situ",
+    "AddRMSNormFunction",
+    "add_rms_norm",
+    "situ_glu_rms_norm_fwd",
+    "situ_glu_rms_norm_fwd_mxfp8",
+    "situ_glu_rms_norm_bwd",
+    "situ_glu_moe_fwd",
+    "situ_glu_nvfp4_quantize",
+    "situ_glu_nvfp4_dequantize",
+    "situ_glu_nvfp4_gemm",
 ]

@@ -55,6 +55,19 @@ SIGNATURES = {
     "situ_glu_fc2_dgrad_workspace_bytes": (_SZ, [_I64, _I64, _INT]),
     "situ_attn_res_fwd": (_INT, [_VP, _I64, _I64, _I64, _VP, _I64, _INT, _I64, _I64, _VP, _INT, _VP, _INT, _DBL,
                                  _VP, _INT, _I64, _VP]),
+    "situ_glu_rms_norm_fwd": (_INT, [_VP, _INT, _I64, _I64, _I64, _VP, _I64, _VP, _INT, _DBL, _VP, _I64, _VP, _I64, _VP]),
+    "situ_glu_rms_norm_fwd_mxfp8": (_INT, [_VP, _INT, _I64, _I64, _I64, _VP, _I64, _VP, _INT, _DBL, _VP, _I64, _VP, _I64,
+                                           _VP, _I64, _INT, _VP]),
+    "situ_glu_rms_norm_bwd": (_INT, [_VP, _I64, _VP, _I64, _VP, _INT, _I64, _I64, _I64, _VP, _INT, _DBL, _VP, _I64, _VP,
+                                     _VP, _SZ, _VP]),
+    "situ_glu_rms_norm_bwd_workspace_bytes": (_SZ, [_I64, _I64, _INT]),
+    "situ_glu_moe_fwd": (_INT, [_VP, _I64, _I64, _I64, _VP, _I64, _I64, _VP, _INT, _I64, _VP, _I64, _I64, _I64, _VP, _I64,
+                                _DBL, _INT, _DBL, _VP, _I64, _VP, _SZ, _VP]),
+    "situ_glu_moe_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I64]),
+    "situ_glu_nvfp4_quantize": (_INT, [_VP, _INT, _I64, _I64, _I64, _VP, _I64, _VP, _I64, _VP, _INT, _VP]),
+    "situ_glu_nvfp4_dequantize": (_INT, [_VP, _I64, _VP, _I64, _VP, _I64, _I64, _VP, _INT, _I64, _VP]),
+    "situ_glu_nvfp4_gemm": (_INT, [_VP, _I64, _VP, _I64, _VP, _I64, _I64, _VP, _I64, _VP, _I64, _VP, _I64, _I64, _I64, _VP,
+                                   _VP, _INT, _I64, _VP]),
     "situ_glu_bwd_workspace_bytes": (_SZ, [_I64, _I64, _INT, _INT]),
     "situ_glu_status_string": (ctypes.c_char_p, [_INT]),
     "situ_glu_last_error": (ctypes.c_char_p, []),
@@ -191,6 +204,65 @@ def situ_attn_res_fwd(blocks, nblocks, block_row_stride, block_stride, prefix, p
     return lib().situ_attn_res_fwd(blocks, nblocks, block_row_stride, block_stride, prefix, prefix_row_stride, dtype,
                                    tokens, hidden, norm_weight, norm_dtype, proj_weight, proj_dtype, variance_epsilon,
                                    out, out_dtype, out_row_stride, stream)
+
+
+def situ_glu_rms_norm_fwd(x, dtype, tokens, hidden, x_row_stride, residual, residual_row_stride, weight, weight_dtype,
+                          epsilon, h, h_row_stride, y, y_row_stride, stream) -> int:
+    return lib().situ_glu_rms_norm_fwd(x, dtype, tokens, hidden, x_row_stride, residual, residual_row_stride, weight,
+                                       weight_dtype, epsilon, h, h_row_stride, y, y_row_stride, stream)
+
+
+def situ_glu_rms_norm_fwd_mxfp8(x, dtype, tokens, hidden, x_row_stride, residual, residual_row_stride, weight,
+                                weight_dtype, epsilon, h, h_row_stride, y_data, y_data_row_stride, y_scale,
+                                y_scale_row_stride, rule, stream) -> int:
+    return lib().situ_glu_rms_norm_fwd_mxfp8(x, dtype, tokens, hidden, x_row_stride, residual, residual_row_stride,
+                                             weight, weight_dtype, epsilon, h, h_row_stride, y_data,
+                                             y_data_row_stride, y_scale, y_scale_row_stride, rule, stream)
+
+
+def situ_glu_rms_norm_bwd(grad_y, grad_y_row_stride, grad_h, grad_h_row_stride, h, dtype, tokens, hidden, h_row_stride,
+                          weight, weight_dtype, epsilon, d_x, d_x_row_stride, d_weight, workspace, workspace_bytes,
+                          stream) -> int:
+    return lib().situ_glu_rms_norm_bwd(grad_y, grad_y_row_stride, grad_h, grad_h_row_stride, h, dtype, tokens, hidden,
+                                       h_row_stride, weight, weight_dtype, epsilon, d_x, d_x_row_stride, d_weight,
+                                       workspace, workspace_bytes, stream)
+
+
+def situ_glu_rms_norm_bwd_workspace_bytes(tokens, hidden, want_dweight) -> int:
+    return lib().situ_glu_rms_norm_bwd_workspace_bytes(tokens, hidden, want_dweight)
+
+
+def situ_glu_moe_fwd(x, tokens, hidden, x_row_stride, topk_ids, topk, topk_ids_row_stride, topk_weights, weights_dtype,
+                     topk_weights_row_stride, w1, experts, inter, w1_row_stride, w2, w2_row_stride, beta,
+                     has_linear_beta, linear_beta, y, y_row_stride, workspace, workspace_bytes, stream) -> int:
+    return lib().situ_glu_moe_fwd(x, tokens, hidden, x_row_stride, topk_ids, topk, topk_ids_row_stride, topk_weights,
+                                  weights_dtype, topk_weights_row_stride, w1, experts, inter, w1_row_stride, w2,
+                                  w2_row_stride, beta, has_linear_beta, linear_beta, y, y_row_stride, workspace,
+                                  workspace_bytes, stream)
+
+
+def situ_glu_moe_workspace_bytes(tokens, topk, hidden, inter) -> int:
+    return lib().situ_glu_moe_workspace_bytes(tokens, topk, hidden, inter)
+
+
+def situ_glu_nvfp4_quantize(x, dtype, rows, cols, x_row_stride, data, data_row_stride, scale, scale_row_stride, amax,
+                            amax_given, stream) -> int:
+    return lib().situ_glu_nvfp4_quantize(x, dtype, rows, cols, x_row_stride, data, data_row_stride, scale,
+                                         scale_row_stride, amax, amax_given, stream)
+
+
+def situ_glu_nvfp4_dequantize(data, data_row_stride, scale, scale_row_stride, amax, rows, cols, out, dtype,
+                              out_row_stride, stream) -> int:
+    return lib().situ_glu_nvfp4_dequantize(data, data_row_stride, scale, scale_row_stride, amax, rows, cols, out, dtype,
+                                           out_row_stride, stream)
+
+
+def situ_glu_nvfp4_gemm(a_data, a_data_row_stride, a_scale, a_scale_row_stride, a_amax, tokens, k, w_data,
+                        w_data_row_stride, w_scale, w_scale_row_stride, w_amax, w_amax_stride, experts, n, offsets,
+                        out, out_dtype, out_row_stride, stream) -> int:
+    return lib().situ_glu_nvfp4_gemm(a_data, a_data_row_stride, a_scale, a_scale_row_stride, a_amax, tokens, k, w_data,
+                                     w_data_row_stride, w_scale, w_scale_row_stride, w_amax, w_amax_stride, experts, n,
+                                     offsets, out, out_dtype, out_row_stride, stream)
 
 
 def situ_glu_bwd_no_alloc(gate_up, dtype, tokens, inter, gate_up_row_stride, rw, rw_dtype, rw_mode, rw_stride,

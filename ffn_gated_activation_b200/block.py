@@ -1,0 +1,404 @@
+"""Tensor-level binding of the operators around the activation in an expert
+block: the residual RMS norm in front of it, the whole expert layer of a
+decoding step, and NVFP4 storage and products.
+
+As in functional.py, PyTorch supplies device memory and the stream, and every
+step of the computation runs in the library's kernels.  Each call runs on the
+device of its tensors, whichever is current; with ``stream`` given, what it
+allocates belongs to that stream.
+"""
+from __future__ import annotations
+
+import math
+
+import torch
+from torch.autograd.function import once_differentiable
+
+from . import abi
+from .functional import (DEFAULT_BETA, DEFAULT_LINEAR_BETA, _check_beta, _dtype_code, _given, _mx_buffers, _mx_rule)
+
+DEFAULT_EPSILON = 1e-6
+
+
+class _Scope:
+    """The device (and, if given, the stream) a call runs on; yields the stream's handle."""
+
+    __slots__ = ("device", "stream", "entered")
+
+    def __init__(self, device, stream):
+        self.device, self.stream, self.entered = device, stream, []
+
+    def __enter__(self) -> int:
+        if self.stream is not None and self.stream.device != self.device:
+            raise ValueError(f"stream is on {self.stream.device}, the tensors on {self.device}")
+        if self.device.index != torch.cuda.current_device():
+            self.entered.append(torch.cuda.device(self.device))
+        if self.stream is not None:
+            self.entered.append(torch.cuda.stream(self.stream))
+        for c in self.entered:
+            c.__enter__()
+        return int(torch.cuda.current_stream().cuda_stream)
+
+    def __exit__(self, *exc):
+        while self.entered:
+            self.entered.pop().__exit__(*exc)
+        return False
+
+
+def _cuda(t: torch.Tensor, what: str) -> torch.device:
+    if t.device.type != "cuda":
+        raise ValueError(f"{what} must be a CUDA tensor")
+    return t.device
+
+
+def _same_device(device, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} must be on {device}, got {t.device}")
+
+
+def _matrix(t: torch.Tensor, cols: int) -> torch.Tensor:
+    """[..., cols] as [rows, cols] with each row's elements adjacent and rows
+    not overlapping (copied where they are not)."""
+    t2 = t if t.dim() == 2 else t.reshape(-1, cols)
+    if t2.numel() and (t2.stride(1) != 1 or (t2.shape[0] > 1 and t2.stride(0) < cols)):
+        t2 = t2.contiguous()
+    return t2
+
+
+def _pitch(t2: torch.Tensor) -> int:
+    return t2.stride(0) if t2.shape[0] > 1 else t2.shape[1]
+
+
+def _ptr(t):
+    return t.data_ptr() if t is not None else None
+
+
+def _check_eps(eps):
+    if not (isinstance(eps, (int, float)) and math.isfinite(eps) and eps >= 0):
+        raise ValueError(f"eps must be a finite number >= 0, got {eps!r}")
+
+
+# ---- residual addition + RMS norm -------------------------------------------------
+
+def _norm_args(x, weight, eps, residual):
+    """Checks of a norm's inputs; returns (device, dtype code, weight dtype code, hidden)."""
+    device = _cuda(x, "x")
+    _check_eps(eps)
+    if x.dim() < 1:
+        raise ValueError("x must be [..., hidden]")
+    hidden = x.shape[-1]
+    dtype = _dtype_code(x, "x")
+    wdtype = _dtype_code(weight, "weight")
+    if weight.dim() != 1 or weight.shape[0] != hidden:
+        raise ValueError(f"weight must be [{hidden}], got {tuple(weight.shape)}")
+    _same_device(device, weight=weight, residual=residual)
+    if residual is not None and (residual.shape != x.shape or residual.dtype != x.dtype):
+        raise ValueError(f"residual must have x's shape {tuple(x.shape)} and dtype {x.dtype}, got "
+                         f"{tuple(residual.shape)} {residual.dtype}")
+    return device, dtype, wdtype, hidden
+
+
+def _like(out, x, what):
+    """An output of x's shape and dtype, allocated when not given; (tensor, 2-D view)."""
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        return out, out.view(-1, x.shape[-1]) if x.dim() != 2 else out
+    return out, _given(out, tuple(x.shape), x.device, what, x.dtype)
+
+
+def situ_glu_rms_norm_fwd(x: torch.Tensor, weight: torch.Tensor, eps: float = DEFAULT_EPSILON,
+                          residual: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                          h_out: torch.Tensor | None = None, stream=None):
+    """h = x + residual (rounded to x's dtype), y = h / sqrt(mean h^2 + eps) * weight
+    over the last axis of x [..., hidden].  Returns (y, h); h is None without a
+    residual.  ``weight`` [hidden] in bf16 or fp32; y and h in x's dtype."""
+    device, dtype, wdtype, hidden = _norm_args(x, weight, eps, residual)
+    if residual is None and h_out is not None:
+        raise ValueError("h_out needs a residual")
+    with _Scope(device, stream) as handle:
+        x2, w, h, h2 = _matrix(x, hidden), weight.contiguous(), None, None
+        y, y2 = _like(out, x, "out")
+        r2 = None
+        if residual is not None:
+            r2 = _matrix(residual, hidden)
+            h, h2 = _like(h_out, x, "h_out")
+        st = abi.situ_glu_rms_norm_fwd(x2.data_ptr(), dtype, x2.shape[0], hidden, _pitch(x2), _ptr(r2),
+                                       _pitch(r2) if r2 is not None else 0, w.data_ptr(), wdtype, float(eps), _ptr(h2),
+                                       _pitch(h2) if h2 is not None else 0, y2.data_ptr(), _pitch(y2), handle)
+    abi.check(st, "situ_glu_rms_norm_fwd")
+    return y, h
+
+
+def situ_glu_rms_norm_fwd_mxfp8(x: torch.Tensor, weight: torch.Tensor, eps: float = DEFAULT_EPSILON,
+                                residual: torch.Tensor | None = None, rule="ocp", data=None, scale=None,
+                                h_out: torch.Tensor | None = None, stream=None):
+    """The forward with MXFP8 rows (format and rules of situ_glu_fwd_mxfp8),
+    quantised from the fp32 values: returns (E4M3 codes [..., hidden], scale
+    bytes [..., hidden / 32], h or None).  hidden must be a multiple of 32."""
+    device, dtype, wdtype, hidden = _norm_args(x, weight, eps, residual)
+    if residual is None and h_out is not None:
+        raise ValueError("h_out needs a residual")
+    if hidden % 32:
+        raise ValueError(f"hidden must be a multiple of 32, got {hidden}")
+    with _Scope(device, stream) as handle:
+        x2, w, h, h2 = _matrix(x, hidden), weight.contiguous(), None, None
+        data, scale, d2, s2 = _mx_buffers(tuple(x.shape[:-1]), hidden, device, data, scale)
+        r2 = None
+        if residual is not None:
+            r2 = _matrix(residual, hidden)
+            h, h2 = _like(h_out, x, "h_out")
+        st = abi.situ_glu_rms_norm_fwd_mxfp8(x2.data_ptr(), dtype, x2.shape[0], hidden, _pitch(x2), _ptr(r2),
+                                             _pitch(r2) if r2 is not None else 0, w.data_ptr(), wdtype, float(eps),
+                                             _ptr(h2), _pitch(h2) if h2 is not None else 0, d2.data_ptr(), _pitch(d2),
+                                             s2.data_ptr(), _pitch(s2), _mx_rule(rule), handle)
+    abi.check(st, "situ_glu_rms_norm_fwd_mxfp8")
+    return data, scale, h
+
+
+def situ_glu_rms_norm_bwd(grad_y: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, eps: float = DEFAULT_EPSILON,
+                          grad_h: torch.Tensor | None = None, want_dw: bool = True,
+                          d_x: torch.Tensor | None = None, d_weight: torch.Tensor | None = None,
+                          workspace: torch.Tensor | None = None, stream=None):
+    """Gradients of the forward from its h (x where there was no residual):
+    returns (d_x, d_weight or None).  d_x is the gradient of x and of the
+    residual; ``grad_h`` is the gradient that reaches h by itself (the residual
+    stream's).  d_weight is summed in fp32 in an order that the shape fixes."""
+    device, dtype, wdtype, hidden = _norm_args(h, weight, eps, None)
+    for name, g in (("grad_y", grad_y), ("grad_h", grad_h)):
+        if g is not None and (g.shape != h.shape or g.dtype != h.dtype):
+            raise ValueError(f"{name} must have h's shape {tuple(h.shape)} and dtype {h.dtype}, got "
+                             f"{tuple(g.shape)} {g.dtype}")
+    _same_device(device, grad_y=grad_y, grad_h=grad_h)
+    with _Scope(device, stream) as handle:
+        h2, g2, w = _matrix(h, hidden), _matrix(grad_y, hidden), weight.contiguous()
+        gh2 = _matrix(grad_h, hidden) if grad_h is not None else None
+        d_x, dx2 = _like(d_x, h, "d_x")
+        if not want_dw:
+            d_weight = None
+        elif d_weight is None:
+            d_weight = torch.empty(hidden, dtype=weight.dtype, device=device)
+        elif tuple(d_weight.shape) != (hidden,) or d_weight.dtype != weight.dtype or d_weight.device != device or \
+                not d_weight.is_contiguous():
+            raise ValueError(f"d_weight must be a contiguous {weight.dtype} [{hidden}] on {device}")
+        tokens = h2.shape[0]
+        ws = abi.situ_glu_rms_norm_bwd_workspace_bytes(tokens, hidden, int(want_dw))
+        if ws:
+            workspace = _workspace(workspace, ws, device)
+        st = abi.situ_glu_rms_norm_bwd(g2.data_ptr(), _pitch(g2), _ptr(gh2), _pitch(gh2) if gh2 is not None else 0,
+                                       h2.data_ptr(), dtype, tokens, hidden, _pitch(h2), w.data_ptr(), wdtype, float(eps),
+                                       dx2.data_ptr(), _pitch(dx2), _ptr(d_weight), _ptr(workspace) if ws else None, ws,
+                                       handle)
+    abi.check(st, "situ_glu_rms_norm_bwd")
+    return d_x, d_weight
+
+
+def _workspace(given, nbytes: int, device) -> torch.Tensor:
+    """The caller's scratch, or one allocated for this call."""
+    if given is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    if given.device != device or not given.is_contiguous() or given.numel() * given.element_size() < nbytes:
+        raise ValueError(f"workspace must be contiguous, on {device}, of at least {nbytes} bytes")
+    return given
+
+
+class AddRMSNormFunction(torch.autograd.Function):
+    """Residual addition + RMS norm; saves h and weight only (h is an output)."""
+
+    @staticmethod
+    def forward(ctx, x, weight, eps, residual):
+        ctx.set_materialize_grads(False)
+        y, h = situ_glu_rms_norm_fwd(x, weight, eps, residual)
+        ctx.eps = eps
+        ctx.has_residual = residual is not None
+        ctx.save_for_backward(h if residual is not None else x, weight)
+        return (y, h) if residual is not None else y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, grad_y, grad_h=None):
+        h, weight = ctx.saved_tensors
+        want_x = ctx.needs_input_grad[0] or ctx.needs_input_grad[3]
+        want_dw = ctx.needs_input_grad[1]
+        if grad_y is None:  # nothing reached y: the stream's gradient passes through
+            return grad_h, torch.zeros_like(weight) if want_dw else None, None, grad_h if ctx.has_residual else None
+        d_x, d_w = situ_glu_rms_norm_bwd(grad_y, h, weight, ctx.eps, grad_h=grad_h, want_dw=want_dw)
+        if not want_x:
+            d_x = None
+        return d_x, d_w, None, d_x if ctx.has_residual else None
+
+
+def add_rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = DEFAULT_EPSILON,
+                 residual: torch.Tensor | None = None):
+    """Differentiable residual addition + RMS norm over the last axis: y, or
+    (y, h) with a residual (h = x + residual, the residual stream from here on)."""
+    return AddRMSNormFunction.apply(x, weight, eps, residual)
+
+
+# ---- the expert layer of a decoding step ------------------------------------------
+
+def situ_glu_moe_fwd(x: torch.Tensor, topk_ids: torch.Tensor, topk_weights: torch.Tensor | None, w1: torch.Tensor,
+                     w2: torch.Tensor, beta: float = DEFAULT_BETA, linear_beta: float | None = DEFAULT_LINEAR_BETA,
+                     out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                     stream=None) -> torch.Tensor:
+    """y[t] = sum over t's experts of W2_e (SiTU-GLU(W1_e x[t]) w[t, e]) for up to
+    64 tokens.  x: bf16 [T, H]; topk_ids: int64 [T, k], an id outside
+    [0, E) is skipped (-1: an empty slot); topk_weights: [T, k] or None (1);
+    w1: bf16 [E, 2I, H] (I gate rows, then I up rows); w2: bf16 [E, H, I].
+    Returns bf16 [T, H].  Calls that overlap on the GPU need a ``workspace``
+    each (situ_glu_moe_workspace_bytes; allocated when not given)."""
+    _check_beta(beta, linear_beta)
+    device = _cuda(x, "x")
+    for t, name in ((x, "x"), (w1, "w1"), (w2, "w2")):
+        if t.dtype != torch.bfloat16:
+            raise TypeError(f"{name} must be bfloat16, got {t.dtype}")
+    if x.dim() != 2 or topk_ids.dim() != 2 or topk_ids.shape[0] != x.shape[0]:
+        raise ValueError(f"x must be [T, H] and topk_ids [T, k], got {tuple(x.shape)} and {tuple(topk_ids.shape)}")
+    if topk_ids.dtype != torch.int64:
+        raise TypeError(f"topk_ids must be int64, got {topk_ids.dtype}")
+    tokens, hidden = x.shape
+    topk = topk_ids.shape[1]
+    if w1.dim() != 3 or w2.dim() != 3 or w1.shape[2] != hidden or w2.shape[1] != hidden or \
+            w1.shape[0] != w2.shape[0] or w1.shape[1] != 2 * w2.shape[2]:
+        raise ValueError(f"w1 {tuple(w1.shape)} and w2 {tuple(w2.shape)} must be [E, 2I, {hidden}] and [E, {hidden}, I]")
+    experts, inter = w2.shape[0], w2.shape[2]
+    if topk_weights is not None and topk_weights.shape != topk_ids.shape:
+        raise ValueError(f"topk_weights must be {tuple(topk_ids.shape)}, got {tuple(topk_weights.shape)}")
+    _same_device(device, topk_ids=topk_ids, topk_weights=topk_weights, w1=w1, w2=w2)
+    wdtype = _dtype_code(topk_weights, "topk_weights") if topk_weights is not None else abi.SITU_DTYPE_F32
+    with _Scope(device, stream) as handle:
+        x2, ids = _matrix(x, hidden), _matrix(topk_ids, topk)
+        tw = _matrix(topk_weights, topk) if topk_weights is not None else None
+        w1f, w2f = _matrix(w1, hidden), _matrix(w2, inter)
+        if out is None:
+            out = torch.empty(tokens, hidden, dtype=torch.bfloat16, device=device)
+            o2 = out
+        else:
+            o2 = _given(out, (tokens, hidden), device, "out", torch.bfloat16)
+        ws = abi.situ_glu_moe_workspace_bytes(tokens, topk, hidden, inter)
+        if ws:
+            workspace = _workspace(workspace, ws, device)
+        st = abi.situ_glu_moe_fwd(x2.data_ptr(), tokens, hidden, _pitch(x2), ids.data_ptr(), topk, _pitch(ids), _ptr(tw),
+                                  wdtype, _pitch(tw) if tw is not None else topk, w1f.data_ptr(), experts, inter,
+                                  _pitch(w1f), w2f.data_ptr(), _pitch(w2f), float(beta), int(linear_beta is not None),
+                                  float(linear_beta) if linear_beta is not None else 0.0, o2.data_ptr(), _pitch(o2),
+                                  _ptr(workspace) if ws else None, ws, handle)
+    abi.check(st, "situ_glu_moe_fwd")
+    return out
+
+
+# ---- NVFP4 storage and product ----------------------------------------------------
+
+def _amax_word(amax, device, what="amax"):
+    if amax.dtype != torch.float32 or amax.numel() != 1 or amax.device != device:
+        raise ValueError(f"{what} must be one float32 element on {device}")
+    return amax
+
+
+def situ_glu_nvfp4_quantize(x: torch.Tensor, amax: torch.Tensor | None = None, data=None, scale=None,
+                            amax_out: torch.Tensor | None = None, amax_only: bool = False, stream=None):
+    """NVFP4 of x [..., C] (bf16 or fp32, C a multiple of 16), in the format of
+    situ_glu_fwd_nvfp4: returns (packed E2M1 codes [..., C / 2] uint8, E4M3
+    block scales [..., C / 16], amax [1]).  Every code and scale is the
+    correctly rounded one.  ``amax``: a known tensor maximum; otherwise it is
+    computed into ``amax_out``.  ``amax_only``: (None, None, amax)."""
+    device = _cuda(x, "x")
+    dtype = _dtype_code(x, "x")
+    if x.dim() < 1 or x.shape[-1] % 16 or x.shape[-1] == 0:
+        raise ValueError(f"the last axis of x must be a positive multiple of 16, got {tuple(x.shape)}")
+    cols, lead = x.shape[-1], tuple(x.shape[:-1])
+    if amax_only and amax is not None:
+        raise ValueError("amax_only computes the tensor maximum: do not pass one")
+    with _Scope(device, stream) as handle:
+        x2, d2, s2 = _matrix(x, cols), None, None
+        if not amax_only:
+            if data is None:
+                data = torch.empty(lead + (cols // 2,), dtype=torch.uint8, device=device)
+            d2 = _given(data, lead + (cols // 2,), device, "NVFP4 data")
+            if scale is None:
+                scale = torch.empty(lead + (cols // 16,), dtype=torch.float8_e4m3fn, device=device)
+            s2 = _given(scale, lead + (cols // 16,), device, "NVFP4 scale")
+        given = amax is not None
+        if amax is None:
+            amax = amax_out if amax_out is not None else torch.empty(1, dtype=torch.float32, device=device)
+        _amax_word(amax, device)
+        st = abi.situ_glu_nvfp4_quantize(x2.data_ptr(), dtype, x2.shape[0], cols, _pitch(x2), _ptr(d2),
+                                         _pitch(d2) if d2 is not None else cols // 2, _ptr(s2),
+                                         _pitch(s2) if s2 is not None else cols // 16, amax.data_ptr(),
+                                         2 if amax_only else int(given), handle)
+    abi.check(st, "situ_glu_nvfp4_quantize")
+    return (None, None, amax) if amax_only else (data, scale, amax)
+
+
+def _codes(data, scale, what):
+    """Checks of NVFP4 codes and scales [..., C / 2] and [..., C / 16]; returns C."""
+    if data.element_size() != 1 or scale.element_size() != 1:
+        raise TypeError(f"{what}: codes and scales are one byte an element")
+    if data.dim() < 1 or scale.shape[:-1] != data.shape[:-1] or data.shape[-1] != 8 * scale.shape[-1]:
+        raise ValueError(f"{what}: codes {tuple(data.shape)} and scales {tuple(scale.shape)} must be "
+                         "[..., C / 2] and [..., C / 16]")
+    return 2 * data.shape[-1]
+
+
+def situ_glu_nvfp4_dequantize(data: torch.Tensor, scale: torch.Tensor, amax: torch.Tensor,
+                              dtype: torch.dtype = torch.bfloat16, out: torch.Tensor | None = None,
+                              stream=None) -> torch.Tensor:
+    """The values q * scale * amax / 2688 that NVFP4 codes stand for, [..., C] in ``dtype``."""
+    device = _cuda(data, "data")
+    cols = _codes(data, scale, "situ_glu_nvfp4_dequantize")
+    _same_device(device, scale=scale)
+    _amax_word(amax, device)
+    shape = tuple(data.shape[:-1]) + (cols,)
+    with _Scope(device, stream) as handle:
+        d2, s2 = _matrix(data, cols // 2), _matrix(scale, cols // 16)
+        if out is None:
+            out = torch.empty(shape, dtype=dtype, device=device)
+        o2 = _given(out, shape, device, "out", dtype)
+        st = abi.situ_glu_nvfp4_dequantize(d2.data_ptr(), _pitch(d2), s2.data_ptr(), _pitch(s2), amax.data_ptr(),
+                                           d2.shape[0], cols, o2.data_ptr(), _dtype_code(out, "out"), _pitch(o2), handle)
+    abi.check(st, "situ_glu_nvfp4_dequantize")
+    return out
+
+
+def situ_glu_nvfp4_gemm(a, w, offsets: torch.Tensor | None = None, out_dtype: torch.dtype = torch.bfloat16,
+                        out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Grouped NVFP4 product on the fp4 tensor cores: rows [offsets[e],
+    offsets[e + 1]) of a times expert e's weight transposed.
+
+    a, w: (codes, scales, amax) as situ_glu_nvfp4_quantize and
+    situ_glu_fwd_nvfp4 return them; a of [T, K], w of [E, N, K] (or [N, K]: one
+    expert), its amax one element or [E].  offsets: int64 [E + 1], or None with
+    one expert (every row).  Returns [T, N] in out_dtype (bf16 or fp32); rows
+    outside every expert are left as they are in ``out`` (uninitialised when
+    out is None)."""
+    (ad, asc, aa), (wd, wsc, wa) = a, w
+    device = _cuda(ad, "a")
+    k = _codes(ad, asc, "a")
+    if _codes(wd, wsc, "w") != k or ad.dim() != 2 or wd.dim() not in (2, 3):
+        raise ValueError(f"a must hold [T, K] and w [E, N, K] or [N, K], got codes {tuple(ad.shape)} and {tuple(wd.shape)}")
+    experts, n = (wd.shape[0], wd.shape[1]) if wd.dim() == 3 else (1, wd.shape[0])
+    _same_device(device, a_scale=asc, w_data=wd, w_scale=wsc, w_amax=wa, offsets=offsets)
+    _amax_word(aa, device, "a's amax")
+    if wa.dtype != torch.float32 or wa.numel() not in (1, experts):
+        raise ValueError(f"w's amax must be 1 or {experts} float32 elements")
+    if offsets is None:
+        if experts != 1:
+            raise ValueError(f"offsets are needed with {experts} experts")
+    elif offsets.dtype != torch.int64 or offsets.dim() != 1 or offsets.numel() != experts + 1:
+        raise ValueError(f"offsets must be int64 [{experts + 1}]")
+    if out_dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"out_dtype must be bfloat16 or float32, got {out_dtype}")
+    tokens = ad.shape[0]
+    with _Scope(device, stream) as handle:
+        ad, asc = _matrix(ad, k // 2), _matrix(asc, k // 16)
+        wd, wsc, wa = _matrix(wd, k // 2), _matrix(wsc, k // 16), wa.reshape(-1).contiguous()
+        off = offsets.contiguous() if offsets is not None else None
+        if out is None:
+            out = torch.empty(tokens, n, dtype=out_dtype, device=device)
+        o2 = _given(out, (tokens, n), device, "out", out_dtype)
+        st = abi.situ_glu_nvfp4_gemm(ad.data_ptr(), _pitch(ad), asc.data_ptr(), _pitch(asc), aa.data_ptr(), tokens, k,
+                                     wd.data_ptr(), _pitch(wd), wsc.data_ptr(), _pitch(wsc), wa.data_ptr(),
+                                     0 if wa.numel() == 1 else 1, experts, n, _ptr(off), o2.data_ptr(),
+                                     _dtype_code(out, "out"), _pitch(o2), handle)
+    abi.check(st, "situ_glu_nvfp4_gemm")
+    return out

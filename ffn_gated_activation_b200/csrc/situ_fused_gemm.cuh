@@ -13,9 +13,9 @@
 // The fp32 accumulators never leave the chip: G and U (or dY) are never
 // written, only Y (or dG, dU and per-tile d_w partials).
 //
-// Included into situ_glu.cu (anonymous namespace): it uses the library's
-// element arithmetic (fwd_pair_abs, bwd_pair), storage helpers and bounded
-// mbarriers.
+// Included inside an anonymous namespace, after situ_device.cuh: it uses the
+// library's element arithmetic (fwd_pair_abs, bwd_pair), storage helpers and
+// bounded mbarriers.
 //
 // Structure (one CTA per SM, persistent over output tiles):
 //   * a tile is 128 token rows; its B operand is 256 rows of the expert's
@@ -215,14 +215,15 @@ __device__ __forceinline__ Tile decode_tile(int t, const int* first_tile, const 
 // decreasing pair read as empty) and its first tile of BM rows: lane l of the
 // calling warp takes a contiguous run of experts, a warp scan adds the runs'
 // tile counts.
-template <int BM>
+template <int BM, class Args>
 __device__ __forceinline__ void scan_experts(const Args& a, int n_tiles, int lane, int64_t* lo, int64_t* hi,
                                              int* first_tile) {
   const int per = (a.experts + 31) / 32;
   const int e0 = min(a.experts, lane * per), e1 = min(a.experts, e0 + per);
   int count = 0;
   for (int e = e0; e < e1; ++e) {
-    int64_t r0 = a.offsets[e], r1 = a.offsets[e + 1];
+    // no offsets: one expert that has every row
+    int64_t r0 = a.offsets != nullptr ? a.offsets[e] : 0, r1 = a.offsets != nullptr ? a.offsets[e + 1] : a.tokens;
     r0 = r0 < 0 ? 0 : (r0 > a.tokens ? a.tokens : r0);
     r1 = r1 < r0 ? r0 : (r1 > a.tokens ? a.tokens : r1);
     lo[e] = r0;

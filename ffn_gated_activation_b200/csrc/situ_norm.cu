@@ -1,0 +1,576 @@
+// situ_norm.cu -- residual addition + RMS norm in front of the experts
+// (include/situ_glu.h, situ_glu_rms_norm_*): forward with native or MXFP8 rows,
+// and the backward.
+//
+//   h = x + residual (rounded to the storage type),  q = 1 / sqrt(mean h^2 + eps)
+//   y = h q w
+//   d_x = grad_h + q g - h q^3 mean(g h),  g = grad_y w;   d_w = sum_t grad_y h q
+//
+// Every element is read and written once (8 bytes an element in bf16 either
+// way, a dozen operations), so the bound is HBM bandwidth.  A row lives in the
+// registers of its threads between its sum and its output: V 16-byte vectors
+// per thread, thread t holding vectors t, t + n, ... of the row.
+
+#include <initializer_list>
+
+#include "situ_host.cuh"
+
+namespace {
+
+constexpr int64_t kNormMaxRowBytes = 65536;  // eight vectors in each of 512 threads
+// Threads of a CTA with V vectors a thread (row_shape below).
+template <int V>
+constexpr int kNormThreads = V == 8 ? 512 : 256;
+
+struct NormArgs {
+  const char* x;
+  int64_t x_pitch;    // bytes, as every pitch here
+  const char* res;    // NULL: none
+  int64_t res_pitch;
+  const void* w;
+  int w_bf16;
+  char* h;
+  int64_t h_pitch;
+  char* y;
+  int64_t y_pitch;
+  int64_t tokens;
+  int vpr;            // 16-byte vectors of a row
+  float eps, inv_hidden;
+};
+
+// The weights of vector j of a row as fp32 pairs.
+template <typename S>
+__device__ __forceinline__ void norm_weights(const void* w, int bf16, int j, float2 (&c)[S::kPairs]) {
+  if (bf16) {
+    const uint32_t* p = static_cast<const uint32_t*>(w) + static_cast<int64_t>(j) * S::kPairs;
+    uint32_t q[S::kPairs];
+    if constexpr (S::kPairs == 4) {
+      const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
+      q[0] = v.x, q[1] = v.y, q[2] = v.z, q[3] = v.w;
+    } else {
+      const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+      q[0] = v.x, q[1] = v.y;
+    }
+#pragma unroll
+    for (int k = 0; k < S::kPairs; ++k) c[k] = bf16x2_to_f2(q[k]);
+  } else {
+    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(w) + static_cast<int64_t>(j) * 2 * S::kPairs);
+#pragma unroll
+    for (int k = 0; k < S::kPairs; k += 2) {
+      const float4 v = __ldg(p + k / 2);
+      c[k] = make_float2(v.x, v.y);
+      c[k + 1] = make_float2(v.z, v.w);
+    }
+  }
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// Sum over the threads of a row, in an order that the row's width alone fixes;
+// every thread gets it.  A row of one warp needs no barrier; otherwise the CTA
+// is the row, and `slot` alternates between two buffers so that one barrier a
+// call suffices.
+__device__ __forceinline__ float row_sum(float v, float* slot, int warps) {
+  v = warp_sum(v);
+  if (warps == 1) return v;
+  if ((threadIdx.x & 31) == 0) slot[threadIdx.x >> 5] = v;
+  __syncthreads();
+  const int lane = threadIdx.x & 31;
+  return warp_sum(lane < warps ? slot[lane] : 0.0f);
+}
+__device__ __forceinline__ float2 row_sum2(float2 v, float2* slot, int warps) {
+  v.x = warp_sum(v.x);
+  v.y = warp_sum(v.y);
+  if (warps == 1) return v;
+  if ((threadIdx.x & 31) == 0) slot[threadIdx.x >> 5] = v;
+  __syncthreads();
+  const int lane = threadIdx.x & 31;
+  const float2 p = lane < warps ? slot[lane] : make_float2(0.0f, 0.0f);
+  return make_float2(warp_sum(p.x), warp_sum(p.y));
+}
+
+// h = x + r in the storage type.
+template <typename S>
+__device__ __forceinline__ uint4 add_vec(const uint4& x, const uint4& r) {
+  uint4 h;
+#pragma unroll
+  for (int p = 0; p < S::kPairs; ++p) S::put(h, p, add2(as_f2(S::pair(x, p)), as_f2(S::pair(r, p))));
+  return h;
+}
+
+template <typename S, int V, bool RES, bool MX>
+__global__ void __launch_bounds__(kNormThreads<V>) situ_rms_norm_fwd_kernel(const NormArgs a, const MxOut m) {
+  __shared__ float slots[2][32];
+  const int nt = blockDim.x, warps = nt >> 5;
+  int flip = 0;
+  for (int64_t row = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y; row < a.tokens;
+       row += static_cast<int64_t>(gridDim.x) * blockDim.y) {
+    uint4 h[V];
+    float2 acc = make_float2(0.0f, 0.0f);
+    const char* xr = a.x + row * a.x_pitch;
+    const char* rr = RES ? a.res + row * a.res_pitch : nullptr;
+    uint4 r[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int j = threadIdx.x + i * nt;
+      if (j < a.vpr) {
+        h[i] = ld_stream(xr + static_cast<int64_t>(j) * kVecBytes);
+        if (RES) r[i] = ld_stream(rr + static_cast<int64_t>(j) * kVecBytes);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int j = threadIdx.x + i * nt;
+      if (j < a.vpr) {
+        if (RES) {
+          h[i] = add_vec<S>(h[i], r[i]);
+          st_stream(a.h + row * a.h_pitch + static_cast<int64_t>(j) * kVecBytes, h[i]);
+        }
+#pragma unroll
+        for (int p = 0; p < S::kPairs; ++p) {
+          const float2 f = as_f2(S::pair(h[i], p));
+          acc = fma2(f, f, acc);
+        }
+      }
+    }
+    const float ss = row_sum(acc.x + acc.y, slots[flip], warps);
+    flip ^= 1;
+    const float q = rsqrtf(ss * a.inv_hidden + a.eps);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int j = threadIdx.x + i * nt;
+      const bool in = j < a.vpr;
+      float2 y[S::kPairs];
+      if (in) {
+        float2 w[S::kPairs];
+        norm_weights<S>(a.w, a.w_bf16, j, w);
+#pragma unroll
+        for (int p = 0; p < S::kPairs; ++p) y[p] = mul2(mul2(as_f2(S::pair(h[i], p)), splat(q)), w[p]);
+      } else {
+#pragma unroll
+        for (int p = 0; p < S::kPairs; ++p) y[p] = make_float2(0.0f, 0.0f);
+      }
+      if constexpr (MX) {  // every lane takes part in the block maxima
+        mx_store_vec<S>(y, in, m.data + row * m.data_pitch, m.scale + row * m.scale_pitch, MxSlot<S>(j), m.rule);
+      } else if (in) {
+        uint4 o;
+#pragma unroll
+        for (int p = 0; p < S::kPairs; ++p) S::put(o, p, y[p]);
+        st_stream(a.y + row * a.y_pitch + static_cast<int64_t>(j) * kVecBytes, o);
+      }
+    }
+  }
+}
+
+// ---- backward -----------------------------------------------------------------
+// d_weight is a sum over rows.  Chunk c of `chunks` holds rows c, c + chunks,
+// ...; the CTA that has a chunk adds its rows' terms in registers (each thread
+// has its own columns) and writes one fp32 row of partial sums; a second kernel
+// adds the chunks in order.  Both orders depend on the shape alone.
+
+constexpr int kNormChunks = 296;  // two per SM of a B200
+
+struct NormBwdArgs {
+  const char* gy;
+  int64_t gy_pitch;
+  const char* gh;     // NULL: zero
+  int64_t gh_pitch;
+  const char* h;
+  int64_t h_pitch;
+  const void* w;
+  int w_bf16;
+  char* dx;
+  int64_t dx_pitch;
+  float* partials;    // [chunks][hidden], NULL: d_weight not wanted
+  int64_t tokens;
+  int64_t chunks;
+  int vpr;
+  float eps, inv_hidden;
+};
+
+template <typename S, int V>
+__global__ void __launch_bounds__(kNormThreads<V>) situ_rms_norm_bwd_kernel(const NormBwdArgs a) {
+  __shared__ float2 slots[2][32];
+  const int nt = blockDim.x, warps = nt >> 5;
+  int flip = 0;
+  // The thread's own columns' sums: registers, or (rows of eight vectors a
+  // thread, whose sums would spill) the thread's words of shared memory.
+  constexpr bool kInSmem = V == 8;
+  extern __shared__ float2 dw_smem[];
+  float2 dw_reg[kInSmem ? 1 : V][S::kPairs];
+  auto dw = [&](int i, int p) -> float2& {
+    if constexpr (kInSmem) return dw_smem[(i * S::kPairs + p) * nt + threadIdx.x];
+    else return dw_reg[i][p];
+  };
+  for (int64_t c = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y; c < a.chunks;
+       c += static_cast<int64_t>(gridDim.x) * blockDim.y) {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+#pragma unroll
+      for (int p = 0; p < S::kPairs; ++p) dw(i, p) = make_float2(0.0f, 0.0f);
+    for (int64_t row = c; row < a.tokens; row += a.chunks) {
+      uint4 h[V], g[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int j = threadIdx.x + i * nt;
+        if (j < a.vpr) {
+          h[i] = ld_stream(a.h + row * a.h_pitch + static_cast<int64_t>(j) * kVecBytes);
+          g[i] = ld_stream(a.gy + row * a.gy_pitch + static_cast<int64_t>(j) * kVecBytes);
+        }
+      }
+      float2 ss = make_float2(0.0f, 0.0f), gd = ss;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int j = threadIdx.x + i * nt;
+        if (j < a.vpr) {
+          float2 w[S::kPairs];
+          norm_weights<S>(a.w, a.w_bf16, j, w);
+#pragma unroll
+          for (int p = 0; p < S::kPairs; ++p) {
+            const float2 f = as_f2(S::pair(h[i], p));
+            ss = fma2(f, f, ss);
+            gd = fma2(mul2(as_f2(S::pair(g[i], p)), w[p]), f, gd);
+          }
+        }
+      }
+      const float2 sums = row_sum2(make_float2(ss.x + ss.y, gd.x + gd.y), slots[flip], warps);
+      flip ^= 1;
+      const float q = rsqrtf(sums.x * a.inv_hidden + a.eps);
+      const float along = -(q * q * q) * (sums.y * a.inv_hidden);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int j = threadIdx.x + i * nt;
+        if (j < a.vpr) {
+          uint4 o, gh;
+          if (a.gh != nullptr) gh = ld_stream(a.gh + row * a.gh_pitch + static_cast<int64_t>(j) * kVecBytes);
+          float2 w[S::kPairs];
+          norm_weights<S>(a.w, a.w_bf16, j, w);
+#pragma unroll
+          for (int p = 0; p < S::kPairs; ++p) {
+            const float2 f = as_f2(S::pair(h[i], p));
+            const float2 gq = mul2(as_f2(S::pair(g[i], p)), splat(q));
+            float2 d = fma2(gq, w[p], mul2(f, splat(along)));
+            if (a.gh != nullptr) d = add2(d, as_f2(S::pair(gh, p)));
+            S::put(o, p, d);
+            dw(i, p) = fma2(gq, f, dw(i, p));
+          }
+          st_stream(a.dx + row * a.dx_pitch + static_cast<int64_t>(j) * kVecBytes, o);
+        }
+      }
+    }
+    if (a.partials != nullptr) {
+      float* out = a.partials + c * (static_cast<int64_t>(a.vpr) * 2 * S::kPairs);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int j = threadIdx.x + i * nt;
+        if (j < a.vpr) {
+          float4* p = reinterpret_cast<float4*>(out + static_cast<int64_t>(j) * 2 * S::kPairs);
+#pragma unroll
+          for (int k = 0; k < S::kPairs; k += 2)
+            p[k / 2] = make_float4(dw(i, k).x, dw(i, k).y, dw(i, k + 1).x, dw(i, k + 1).y);
+        }
+      }
+    }
+  }
+}
+
+// d_weight[i] = sum of the chunks' partials: 32 columns a CTA, eight groups of
+// chunks side by side, the groups in order at the end.
+constexpr int kNormFinGroups = 8;
+__global__ void __launch_bounds__(32 * kNormFinGroups)
+    situ_rms_norm_dw_kernel(const float* partials, int64_t chunks, int hidden, void* d_w, int bf16) {
+  __shared__ float part[kNormFinGroups][32];
+  const int col = blockIdx.x * 32 + threadIdx.x;
+  float s = 0.0f;
+  if (col < hidden)
+    for (int64_t c = threadIdx.y; c < chunks; c += kNormFinGroups) s += partials[c * hidden + col];
+  part[threadIdx.y][threadIdx.x] = s;
+  __syncthreads();
+  if (threadIdx.y == 0 && col < hidden) {
+    float t = 0.0f;
+#pragma unroll
+    for (int g = 0; g < kNormFinGroups; ++g) t += part[g][threadIdx.x];
+    if (bf16)
+      static_cast<__nv_bfloat16*>(d_w)[col] = __float2bfloat16(t);
+    else
+      static_cast<float*>(d_w)[col] = t;
+  }
+}
+
+// ---- host ---------------------------------------------------------------------
+
+// Threads and vectors per thread of a row of `vpr` vectors.
+struct RowShape {
+  int v, threads, rows;  // rows: rows of one CTA (one warp each)
+};
+RowShape row_shape(int vpr) {
+  if (vpr <= 128) return {vpr <= 32 ? 1 : vpr <= 64 ? 2 : 4, 32, 8};
+  const int v = vpr <= 512 ? 2 : vpr <= 1024 ? 4 : 8;
+  return {v, ((vpr + v - 1) / v + 31) / 32 * 32, 1};
+}
+
+int64_t norm_chunks(int64_t tokens) { return tokens < kNormChunks ? tokens : kNormChunks; }
+
+// Checks shared by the three entry points.
+situ_status_t norm_check(situ_dtype_t dtype, int64_t tokens, int64_t hidden, situ_dtype_t weight_dtype, double eps) {
+  if (!valid_dtype(dtype) || !valid_dtype(weight_dtype))
+    return fail(SITU_ERR_INVALID_ARG, "a dtype is not a situ_dtype_t");
+  if (tokens < 0) return fail(SITU_ERR_INVALID_ARG, "tokens = %lld < 0", (long long)tokens);
+  if (hidden <= 0) return fail(SITU_ERR_INVALID_ARG, "hidden = %lld <= 0", (long long)hidden);
+  if (hidden > kNormMaxRowBytes / elem_size(dtype))
+    return fail(SITU_ERR_UNSUPPORTED, "hidden = %lld exceeds %lld", (long long)hidden,
+                (long long)(kNormMaxRowBytes / elem_size(dtype)));
+  if (!std::isfinite(eps) || eps < 0.0) return fail(SITU_ERR_INVALID_ARG, "epsilon must be finite and >= 0");
+  if ((hidden * elem_size(dtype)) % kVecBytes != 0)
+    return fail(SITU_ERR_MISALIGNED, "hidden * element size (%lld bytes) is not a multiple of 16",
+                (long long)(hidden * elem_size(dtype)));
+  return SITU_OK;
+}
+
+int norm_weight_align(situ_dtype_t dtype, situ_dtype_t weight_dtype) {
+  const int a = kVecBytes / elem_size(dtype) * elem_size(weight_dtype);
+  return a < 16 ? a : 16;
+}
+
+// A row-pitched matrix argument: its stride, extent and alignment.
+struct Matrix {
+  const void* p;
+  int64_t stride, width;
+  int es;
+  const char* name;
+};
+situ_status_t check_matrices(std::initializer_list<Matrix> ms, int64_t rows) {
+  for (const Matrix& m : ms) {
+    if (m.p == nullptr) return fail(SITU_ERR_INVALID_ARG, "%s is NULL", m.name);
+    if (!span_fits(rows, m.stride, m.width, m.es)) return fail(SITU_ERR_INVALID_ARG, "extent of %s overflows int64", m.name);
+    if (!aligned(m.p, 16) || (m.stride * m.es) % 16 != 0)
+      return fail(SITU_ERR_MISALIGNED, "%s base or row pitch not 16-byte aligned", m.name);
+  }
+  return SITU_OK;
+}
+Span span_of(const Matrix& m, int64_t rows) { return matrix_span(m.p, rows, m.stride, m.width, m.es); }
+
+using NormFwdKernel = void (*)(NormArgs, MxOut);
+template <typename S, bool MX>
+NormFwdKernel pick_norm_fwd(int v, bool res) {
+  switch (v) {
+    case 1: return res ? situ_rms_norm_fwd_kernel<S, 1, true, MX> : situ_rms_norm_fwd_kernel<S, 1, false, MX>;
+    case 2: return res ? situ_rms_norm_fwd_kernel<S, 2, true, MX> : situ_rms_norm_fwd_kernel<S, 2, false, MX>;
+    case 4: return res ? situ_rms_norm_fwd_kernel<S, 4, true, MX> : situ_rms_norm_fwd_kernel<S, 4, false, MX>;
+    default: return res ? situ_rms_norm_fwd_kernel<S, 8, true, MX> : situ_rms_norm_fwd_kernel<S, 8, false, MX>;
+  }
+}
+using NormBwdKernel = void (*)(NormBwdArgs);
+template <typename S>
+NormBwdKernel pick_norm_bwd(int v) {
+  switch (v) {
+    case 1: return situ_rms_norm_bwd_kernel<S, 1>;
+    case 2: return situ_rms_norm_bwd_kernel<S, 2>;
+    case 4: return situ_rms_norm_bwd_kernel<S, 4>;
+    default: return situ_rms_norm_bwd_kernel<S, 8>;
+  }
+}
+
+// The forward with native rows (mx == NULL) or MXFP8 rows.
+situ_status_t norm_fwd_entry(const void* x, situ_dtype_t dtype, int64_t tokens, int64_t hidden, int64_t x_row_stride,
+                             const void* residual, int64_t residual_row_stride, const void* weight,
+                             situ_dtype_t weight_dtype, double epsilon, void* h, int64_t h_row_stride, void* y,
+                             int64_t y_row_stride, const MxOut* mx, void* stream, const char* what) {
+  tl_last_error[0] = '\0';
+  situ_status_t st = norm_check(dtype, tokens, hidden, weight_dtype, epsilon);
+  if (st != SITU_OK) return st;
+  if (mx != nullptr) {
+    if (mx->rule != SITU_MX_RULE_OCP && mx->rule != SITU_MX_RULE_CEIL)
+      return fail(SITU_ERR_INVALID_ARG, "rule %d is not a situ_mx_rule_t", mx->rule);
+    if (hidden % kMxBlock != 0)
+      return fail(SITU_ERR_INVALID_ARG, "MXFP8 outputs need hidden a multiple of %d, got %lld", kMxBlock,
+                  (long long)hidden);
+    if (mx->data_pitch < hidden || mx->scale_pitch < hidden / kMxBlock)
+      return fail(SITU_ERR_INVALID_ARG, "MXFP8 data or scale row pitch shorter than a row");
+  }
+  if ((residual == nullptr) != (h == nullptr))
+    return fail(SITU_ERR_INVALID_ARG, "residual and h go together: both or neither may be NULL");
+  const bool res = residual != nullptr;
+  if (x_row_stride < hidden || (res && (residual_row_stride < hidden || h_row_stride < hidden)) ||
+      (mx == nullptr && y_row_stride < hidden))
+    return fail(SITU_ERR_INVALID_ARG, "a row stride is shorter than its row");
+  if (tokens == 0) return SITU_OK;
+  const int es = elem_size(dtype);
+  const Matrix mxx = {x, x_row_stride, hidden, es, "x"};
+  const Matrix mr = res ? Matrix{residual, residual_row_stride, hidden, es, "residual"} : mxx;
+  const Matrix my = mx != nullptr ? Matrix{mx->data, mx->data_pitch, hidden, 1, "y_data"}
+                                  : Matrix{y, y_row_stride, hidden, es, "y"};
+  const Matrix mh = res ? Matrix{h, h_row_stride, hidden, es, "h"} : my;
+  st = check_matrices({mxx, mr, my, mh}, tokens);
+  if (st != SITU_OK) return st;
+  if (mx != nullptr) {
+    if (mx->scale == nullptr) return fail(SITU_ERR_INVALID_ARG, "y_scale is NULL");
+    if (!span_fits(tokens, mx->scale_pitch, hidden / kMxBlock, 1))
+      return fail(SITU_ERR_INVALID_ARG, "extent of y_scale overflows int64");
+  }
+  if (weight == nullptr) return fail(SITU_ERR_INVALID_ARG, "weight is NULL");
+  if (!aligned(weight, norm_weight_align(dtype, weight_dtype)))
+    return fail(SITU_ERR_MISALIGNED, "weight must be %d-byte aligned", norm_weight_align(dtype, weight_dtype));
+  const Span ins[] = {span_of(mxx, tokens), span_of(mr, tokens),
+                      matrix_span(weight, 1, hidden, hidden, elem_size(weight_dtype))};
+  Span outs[3] = {span_of(my, tokens)};
+  int n_outs = 1;
+  if (res) outs[n_outs++] = span_of(mh, tokens);
+  if (mx != nullptr) outs[n_outs++] = matrix_span(mx->scale, tokens, mx->scale_pitch, hidden / kMxBlock, 1);
+  for (int i = 0; i < n_outs; ++i) {
+    for (const Span& s : ins)
+      if (overlap(outs[i], s)) return fail(SITU_ERR_INVALID_ARG, "an output overlaps an input");
+    for (int k = i + 1; k < n_outs; ++k)
+      if (overlap(outs[i], outs[k])) return fail(SITU_ERR_INVALID_ARG, "outputs overlap each other");
+  }
+
+  NormArgs a{};
+  a.x = static_cast<const char*>(x);
+  a.x_pitch = x_row_stride * es;
+  a.res = static_cast<const char*>(residual);
+  a.res_pitch = res ? residual_row_stride * es : 0;
+  a.w = weight;
+  a.w_bf16 = weight_dtype == SITU_DTYPE_BF16;
+  a.h = static_cast<char*>(h);
+  a.h_pitch = res ? h_row_stride * es : 0;
+  a.y = static_cast<char*>(y);
+  a.y_pitch = mx == nullptr ? y_row_stride * es : 0;
+  a.tokens = tokens;
+  a.vpr = static_cast<int>(hidden * es / kVecBytes);
+  a.eps = static_cast<float>(epsilon);
+  a.inv_hidden = static_cast<float>(1.0 / static_cast<double>(hidden));
+  const RowShape rs = row_shape(a.vpr);
+  const bool bf = dtype == SITU_DTYPE_BF16;
+  NormFwdKernel k = mx != nullptr ? (bf ? pick_norm_fwd<Bf16, true>(rs.v, res) : pick_norm_fwd<F32, true>(rs.v, res))
+                                  : (bf ? pick_norm_fwd<Bf16, false>(rs.v, res) : pick_norm_fwd<F32, false>(rs.v, res));
+  int grid = 0;
+  st = launch_grid(reinterpret_cast<const void*>(k), rs.threads * rs.rows, 0, (tokens + rs.rows - 1) / rs.rows, &grid);
+  if (st != SITU_OK) return st;
+  k<<<grid, dim3(rs.threads, rs.rows), 0, static_cast<cudaStream_t>(stream)>>>(a, mx != nullptr ? *mx : MxOut{});
+  return check_launch(what);
+}
+
+}  // namespace
+
+extern "C" {
+
+situ_status_t situ_glu_rms_norm_fwd(const void* x, situ_dtype_t dtype, int64_t tokens, int64_t hidden,
+                                    int64_t x_row_stride, const void* residual, int64_t residual_row_stride,
+                                    const void* weight, situ_dtype_t weight_dtype, double epsilon, void* h,
+                                    int64_t h_row_stride, void* y, int64_t y_row_stride, void* stream) {
+  return norm_fwd_entry(x, dtype, tokens, hidden, x_row_stride, residual, residual_row_stride, weight, weight_dtype,
+                        epsilon, h, h_row_stride, y, y_row_stride, nullptr, stream, "situ_glu_rms_norm_fwd");
+}
+
+situ_status_t situ_glu_rms_norm_fwd_mxfp8(const void* x, situ_dtype_t dtype, int64_t tokens, int64_t hidden,
+                                          int64_t x_row_stride, const void* residual, int64_t residual_row_stride,
+                                          const void* weight, situ_dtype_t weight_dtype, double epsilon, void* h,
+                                          int64_t h_row_stride, void* y_data, int64_t y_data_row_stride,
+                                          void* y_scale, int64_t y_scale_row_stride, situ_mx_rule_t rule,
+                                          void* stream) {
+  const MxOut m{static_cast<char*>(y_data), y_data_row_stride, static_cast<uint8_t*>(y_scale), y_scale_row_stride,
+                static_cast<int>(rule)};
+  return norm_fwd_entry(x, dtype, tokens, hidden, x_row_stride, residual, residual_row_stride, weight, weight_dtype,
+                        epsilon, h, h_row_stride, nullptr, 0, &m, stream, "situ_glu_rms_norm_fwd_mxfp8");
+}
+
+size_t situ_glu_rms_norm_bwd_workspace_bytes(int64_t tokens, int64_t hidden, int want_dweight) {
+  if (!want_dweight || tokens <= 0 || hidden <= 0 || hidden > kNormMaxRowBytes / 2) return 0;
+  return (static_cast<size_t>(norm_chunks(tokens)) * static_cast<size_t>(hidden) * sizeof(float) + 255) / 256 * 256;
+}
+
+situ_status_t situ_glu_rms_norm_bwd(const void* grad_y, int64_t grad_y_row_stride, const void* grad_h,
+                                    int64_t grad_h_row_stride, const void* h, situ_dtype_t dtype, int64_t tokens,
+                                    int64_t hidden, int64_t h_row_stride, const void* weight,
+                                    situ_dtype_t weight_dtype, double epsilon, void* d_x, int64_t d_x_row_stride,
+                                    void* d_weight, void* workspace, size_t workspace_bytes, void* stream) {
+  tl_last_error[0] = '\0';
+  situ_status_t st = norm_check(dtype, tokens, hidden, weight_dtype, epsilon);
+  if (st != SITU_OK) return st;
+  if (grad_y_row_stride < hidden || h_row_stride < hidden || d_x_row_stride < hidden ||
+      (grad_h != nullptr && grad_h_row_stride < hidden))
+    return fail(SITU_ERR_INVALID_ARG, "a row stride is shorter than its row");
+  const int es = elem_size(dtype), wes = elem_size(weight_dtype);
+  if (d_weight != nullptr && !aligned(d_weight, wes))
+    return fail(SITU_ERR_MISALIGNED, "d_weight not aligned to its element");
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (tokens == 0) {
+    if (d_weight != nullptr) {
+      cudaError_t err = cudaMemsetAsync(d_weight, 0, static_cast<size_t>(hidden) * wes, s);
+      if (err != cudaSuccess) return fail(SITU_ERR_CUDA, "cudaMemsetAsync: %s", cudaGetErrorString(err));
+    }
+    return SITU_OK;
+  }
+  const Matrix mg = {grad_y, grad_y_row_stride, hidden, es, "grad_y"};
+  const Matrix mhh = {h, h_row_stride, hidden, es, "h"};
+  const Matrix mgh = grad_h != nullptr ? Matrix{grad_h, grad_h_row_stride, hidden, es, "grad_h"} : mg;
+  const Matrix md = {d_x, d_x_row_stride, hidden, es, "d_x"};
+  st = check_matrices({mg, mhh, mgh, md}, tokens);
+  if (st != SITU_OK) return st;
+  if (weight == nullptr) return fail(SITU_ERR_INVALID_ARG, "weight is NULL");
+  if (!aligned(weight, norm_weight_align(dtype, weight_dtype)))
+    return fail(SITU_ERR_MISALIGNED, "weight must be %d-byte aligned", norm_weight_align(dtype, weight_dtype));
+  const size_t need = situ_glu_rms_norm_bwd_workspace_bytes(tokens, hidden, d_weight != nullptr);
+  if (need > 0) {
+    if (workspace == nullptr || workspace_bytes < need)
+      return fail(SITU_ERR_INVALID_ARG, "workspace of %zu bytes needed, got %zu", need,
+                  workspace == nullptr ? static_cast<size_t>(0) : workspace_bytes);
+    if (!aligned(workspace, 16)) return fail(SITU_ERR_MISALIGNED, "workspace not 16-byte aligned");
+  }
+  const Span ins[] = {span_of(mg, tokens), span_of(mhh, tokens), span_of(mgh, tokens),
+                      matrix_span(weight, 1, hidden, hidden, wes)};
+  Span outs[3] = {span_of(md, tokens)};
+  int n_outs = 1;
+  if (d_weight != nullptr) {
+    outs[n_outs++] = matrix_span(d_weight, 1, hidden, hidden, wes);
+    const uintptr_t ws = reinterpret_cast<uintptr_t>(workspace);
+    outs[n_outs++] = {ws, ws + need};
+  }
+  for (int i = 0; i < n_outs; ++i) {
+    for (const Span& sp : ins)
+      if (overlap(outs[i], sp)) return fail(SITU_ERR_INVALID_ARG, "an output overlaps an input");
+    for (int k = i + 1; k < n_outs; ++k)
+      if (overlap(outs[i], outs[k])) return fail(SITU_ERR_INVALID_ARG, "outputs overlap each other");
+  }
+
+  NormBwdArgs a{};
+  a.gy = static_cast<const char*>(grad_y);
+  a.gy_pitch = grad_y_row_stride * es;
+  a.gh = static_cast<const char*>(grad_h);
+  a.gh_pitch = grad_h != nullptr ? grad_h_row_stride * es : 0;
+  a.h = static_cast<const char*>(h);
+  a.h_pitch = h_row_stride * es;
+  a.w = weight;
+  a.w_bf16 = weight_dtype == SITU_DTYPE_BF16;
+  a.dx = static_cast<char*>(d_x);
+  a.dx_pitch = d_x_row_stride * es;
+  a.partials = d_weight != nullptr ? static_cast<float*>(workspace) : nullptr;
+  a.tokens = tokens;
+  a.chunks = norm_chunks(tokens);
+  a.vpr = static_cast<int>(hidden * es / kVecBytes);
+  a.eps = static_cast<float>(epsilon);
+  a.inv_hidden = static_cast<float>(1.0 / static_cast<double>(hidden));
+  const RowShape rs = row_shape(a.vpr);
+  NormBwdKernel k = dtype == SITU_DTYPE_BF16 ? pick_norm_bwd<Bf16>(rs.v) : pick_norm_bwd<F32>(rs.v);
+  const int smem = rs.v == 8 ? rs.v * rs.threads * (kVecBytes / es) * 4 : 0;
+  if (smem > 48 * 1024) {
+    st = ensure_smem(reinterpret_cast<const void*>(k), smem);
+    if (st != SITU_OK) return st;
+  }
+  int grid = 0;
+  st = launch_grid(reinterpret_cast<const void*>(k), rs.threads * rs.rows, smem, (a.chunks + rs.rows - 1) / rs.rows,
+                   &grid);
+  if (st != SITU_OK) return st;
+  k<<<grid, dim3(rs.threads, rs.rows), smem, s>>>(a);
+  st = check_launch("situ_glu_rms_norm_bwd");
+  if (st != SITU_OK || d_weight == nullptr) return st;
+  situ_rms_norm_dw_kernel<<<static_cast<int>((hidden + 31) / 32), dim3(32, kNormFinGroups), 0, s>>>(
+      a.partials, a.chunks, static_cast<int>(hidden), d_weight, weight_dtype == SITU_DTYPE_BF16);
+  return check_launch("situ_glu_rms_norm_bwd (d_weight)");
+}
+
+}  // extern "C"

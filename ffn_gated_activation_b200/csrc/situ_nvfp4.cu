@@ -1,0 +1,866 @@
+// situ_nvfp4.cu -- NVFP4 storage of any matrix and the grouped NVFP4 product
+// (include/situ_glu.h, situ_glu_nvfp4_*).
+//
+// The format (as situ_glu_fwd_nvfp4 writes it): with A the largest finite |x|
+// of the matrix, each block of 16 elements of a row has the scale
+// s_b = E4M3(amax_b 448 / A) and the codes E2M1(x 2688 / (A s_b)); a code q
+// stands for q s_b A / 2688.
+
+#include "situ_host.cuh"
+
+namespace {
+
+#include "situ_fused_gemm.cuh"
+
+// ---------------------------------------------------------------------------
+// Storage
+// ---------------------------------------------------------------------------
+// One thread has one block of 16 elements: 32 (bf16) or 64 (fp32) bytes in, 8
+// bytes of codes and a scale byte out, no exchange between lanes.  HBM
+// bandwidth is the bound (2.56 bytes an element of bf16 where A is known, 4.56
+// where the first pass has to find it).
+
+constexpr int kStoreThreads = 256;
+
+struct StoreArgs {
+  const char* x;        // quantise: the matrix; dequantise: unused
+  int64_t x_pitch;      // bytes
+  char* data;
+  int64_t data_pitch;
+  uint8_t* scale;
+  int64_t scale_pitch;
+  const float* amax;
+  unsigned int* amax_out;
+  char* out;            // dequantise: the matrix
+  int64_t out_pitch;
+  int64_t rows;
+  int64_t blocks;       // rows * per_row
+  uint32_t per_row;     // blocks of 16 elements
+  int wide;             // the matrix' vectors are 32-byte aligned
+};
+
+// Row and column block of block i.
+__device__ __forceinline__ void block_at(const StoreArgs& a, int64_t i, int64_t& row, uint32_t& col) {
+  if (a.blocks <= 0xffffffffll) {
+    const uint32_t r = static_cast<uint32_t>(i) / a.per_row;
+    row = r;
+    col = static_cast<uint32_t>(i) - r * a.per_row;
+  } else {
+    row = i / a.per_row;
+    col = static_cast<uint32_t>(i - row * a.per_row);
+  }
+}
+
+// The 16 elements of a block as fp32 pairs.
+template <typename S>
+__device__ __forceinline__ void load_block(const char* p, int wide, uint4 (&v)[8 / S::kPairs]) {
+#pragma unroll
+  for (int k = 0; k < 8 / S::kPairs; k += 2) {
+    if (wide) {
+      const U8 u = ld_stream32(p + k * kVecBytes);
+      v[k] = u.a;
+      v[k + 1] = u.b;
+    } else {
+      v[k] = ld_stream(p + k * kVecBytes);
+      v[k + 1] = ld_stream(p + (k + 1) * kVecBytes);
+    }
+  }
+}
+template <typename S>
+__device__ __forceinline__ float2 block_pair(const uint4 (&v)[8 / S::kPairs], int p) {
+  return as_f2(S::pair(v[p / S::kPairs], p % S::kPairs));
+}
+
+// The largest finite magnitude: per-thread maxima, one integer atomicMax per
+// warp (non-negative floats order as integers), so the result is order-free.
+template <typename S>
+__global__ void __launch_bounds__(kStoreThreads) situ_nvfp4_amax_kernel(const StoreArgs a) {
+  float m = 0.0f;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kStoreThreads;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kStoreThreads + threadIdx.x; i < a.blocks; i += step) {
+    int64_t row;
+    uint32_t col;
+    block_at(a, i, row, col);
+    uint4 v[8 / S::kPairs];
+    load_block<S>(a.x + row * a.x_pitch + static_cast<int64_t>(col) * (8 / S::kPairs * kVecBytes), a.wide, v);
+#pragma unroll
+    for (int p = 0; p < 8; ++p) {
+      const float2 f = block_pair<S>(v, p);
+      const float ax = fabsf(f.x), ay = fabsf(f.y);
+      m = ax <= 3.402823466e38f ? fmaxf(m, ax) : m;  // false for NaN and infinity
+      m = ay <= 3.402823466e38f ? fmaxf(m, ay) : m;
+    }
+  }
+  const unsigned int bits = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
+  if ((threadIdx.x & 31) == 0 && bits != 0u) atomicMax(a.amax_out, bits);
+}
+
+// Correctly rounded codes.  The fp32 quotients below are within 2^-22 of the
+// exact ones, so a code can differ from the exact quotient's only where moving
+// the quotient by 2^-20 either way changes it; there the exact products on
+// both sides of the midpoint are compared in double (all of them have at most
+// 36 significant bits).
+constexpr float kUp = 1.0f + 0x1p-20f, kDown = 1.0f - 0x1p-20f;
+
+__device__ __forceinline__ float e4m3_value(uint32_t code) {
+  return __half2float(__half(__nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(code), __NV_E4M3)));
+}
+__device__ __forceinline__ uint32_t e4m3_code(float v) {
+  return __nv_cvt_float_to_fp8(v, __NV_SATFINITE, __NV_E4M3);
+}
+// E4M3(m 448 / big) for m >= 0; r is 448 / big rounded.
+__device__ __forceinline__ uint32_t exact_scale(float m, float big, float r) {
+  const float v = m * r;
+  const uint32_t lo = e4m3_code(v * kDown), hi = e4m3_code(v * kUp);
+  if (lo == hi) return lo;
+  const double mid = 0.5 * (static_cast<double>(e4m3_value(lo)) + static_cast<double>(e4m3_value(hi)));
+  const double left = static_cast<double>(m) * 448.0, right = mid * static_cast<double>(big);
+  return left > right || (left == right && (hi & 1) == 0) ? hi : lo;
+}
+// The magnitude code of E2M1(m 2688 / (big s)) where lo and hi are the codes of
+// the quotient moved down and up.
+__device__ __noinline__ uint32_t exact_code(float m, double big_s, uint32_t lo, uint32_t hi) {
+  const uint32_t twice = 0xC8643210u;  // 2 x the magnitudes 0, .5, 1, 1.5, 2, 3, 4 of the codes 0 .. 6 (6 is 12: C)
+  const double mid = 0.25 * (static_cast<double>((twice >> (4 * lo)) & 15u) + static_cast<double>((twice >> (4 * hi)) & 15u));
+  const double left = static_cast<double>(m) * 2688.0, right = mid * big_s;
+  return left > right || (left == right && (hi & 1) == 0) ? hi : lo;
+}
+
+template <typename S>
+__global__ void __launch_bounds__(kStoreThreads) situ_nvfp4_quantize_kernel(const StoreArgs a) {
+  float big = *a.amax;
+  if (!(big > 0.0f && big <= 3.402823466e38f)) big = 2688.0f;  // S_enc = 1
+  // a tiny A: both sides times 2^80, exactly, so that 448 / A stays finite
+  const float lift = big < 0x1p-60f ? 0x1p80f : 1.0f;
+  big *= lift;
+  const float r448 = 448.0f / big, s_enc = 2688.0f / big;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kStoreThreads;
+  // from the end: what the pass before read last may still be in L2
+  for (int64_t k = static_cast<int64_t>(blockIdx.x) * kStoreThreads + threadIdx.x; k < a.blocks; k += step) {
+    int64_t row;
+    uint32_t col;
+    block_at(a, a.blocks - 1 - k, row, col);
+    uint4 v[8 / S::kPairs];
+    load_block<S>(a.x + row * a.x_pitch + static_cast<int64_t>(col) * (8 / S::kPairs * kVecBytes), a.wide, v);
+    float2 f[8];
+    float m = 0.0f;
+#pragma unroll
+    for (int p = 0; p < 8; ++p) {
+      f[p] = block_pair<S>(v, p);
+      m = max_nan(m, max_nan(fabsf(f[p].x), fabsf(f[p].y)));
+      f[p] = mul2(f[p], splat(lift));
+    }
+    const bool special = !(m <= 3.402823466e38f);
+    const uint32_t sc = special ? 0x7fu : exact_scale(m * lift, big, r448);
+    const float s = special ? 0.0f : e4m3_value(sc);
+    const float inv = s > 0.0f ? s_enc / s : 0.0f;
+    uint32_t q[2] = {0u, 0u};
+    if (!special) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float2 up[4], down[4];
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+          const float2 w = mul2(f[4 * h + p], splat(inv));
+          up[p] = mul2(w, splat(kUp));
+          down[p] = mul2(w, splat(kDown));
+        }
+        const uint32_t hi = e2m1x8(up);
+        uint32_t lo = e2m1x8(down);
+        if (lo != hi) {
+          const double big_s = static_cast<double>(big) * static_cast<double>(s);
+          uint32_t fixed = 0;
+#pragma unroll
+          for (int p = 0; p < 8; ++p) {
+            const uint32_t cl = (lo >> (4 * p)) & 15u, ch = (hi >> (4 * p)) & 15u;
+            const float m1 = fabsf(p & 1 ? f[4 * h + p / 2].y : f[4 * h + p / 2].x);
+            fixed |= (cl == ch ? cl : (exact_code(m1, big_s, cl & 7u, ch & 7u) | (ch & 8u))) << (4 * p);
+          }
+          lo = fixed;
+        }
+        q[h] = lo;
+      }
+    }
+    st_stream8(a.data + row * a.data_pitch + static_cast<int64_t>(col) * 8, make_uint2(q[0], q[1]));
+    a.scale[row * a.scale_pitch + col] = static_cast<uint8_t>(sc);
+  }
+}
+
+// Two E2M1 codes as an exact half2.
+__device__ __forceinline__ float2 e2m1_pair(uint32_t byte) {
+  uint32_t h;
+  asm("{\n\t.reg .b8 b;\n\tcvt.u8.u32 b, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, b;\n\t}" : "=r"(h) : "r"(byte));
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+
+template <typename S>
+__global__ void __launch_bounds__(kStoreThreads) situ_nvfp4_dequantize_kernel(const StoreArgs a) {
+  const double unit = static_cast<double>(*a.amax) / 2688.0;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kStoreThreads;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kStoreThreads + threadIdx.x; i < a.blocks; i += step) {
+    int64_t row;
+    uint32_t col;
+    block_at(a, i, row, col);
+    const uint2 q = ld_stream8(a.data + row * a.data_pitch + static_cast<int64_t>(col) * 8);
+    const float s = static_cast<float>(unit * static_cast<double>(e4m3_value(a.scale[row * a.scale_pitch + col])));
+    uint4 o[8 / S::kPairs];
+#pragma unroll
+    for (int p = 0; p < 8; ++p)
+      S::put(o[p / S::kPairs], p % S::kPairs, mul2(e2m1_pair(((p < 4 ? q.x : q.y) >> (8 * (p & 3))) & 0xffu), splat(s)));
+    char* out = a.out + row * a.out_pitch + static_cast<int64_t>(col) * (8 / S::kPairs * kVecBytes);
+#pragma unroll
+    for (int k = 0; k < 8 / S::kPairs; k += 2) {
+      if (a.wide) {
+        st_stream32(out + k * kVecBytes, o[k], o[k + 1]);
+      } else {
+        st_stream(out + k * kVecBytes, o[k]);
+        st_stream(out + (k + 1) * kVecBytes, o[k + 1]);
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Grouped product
+// ---------------------------------------------------------------------------
+// out[r, n] = sum_k a[r, k] w_e[n, k] on the fp4 tensor cores
+// (tcgen05.mma.kind::mxf4nvf4, a UE4M3 scale per 16 elements of k): the tensor
+// cores multiply the codes by their block scales and add in fp32; the two
+// tensor scales, one number per expert, are applied once in the epilogue.
+//
+// Structure (one CTA per SM, persistent over output tiles of 128 rows and BN
+// columns, numbered expert by expert as in situ_fused_gemm.cuh):
+//   * warp 0 streams the codes with TMA: a stage is 256 elements of k, i.e. a
+//     128-byte swizzle row of A and of B;
+//   * warps 6 .. bring the block scales.  The tensor cores read them from TMEM in
+//     32-lane x 4-column atoms (512 bytes for 128 rows and 64 elements of k:
+//     row r's four scales at lane r % 32, column r / 32), while memory has them
+//     row by row, 16 bytes for a stage's 256 elements.  A lane loads rows l,
+//     l + 32, l + 64, l + 96, and the transposed 4 x 4 words are four 16-byte
+//     shared-memory stores, one per atom, free of bank conflicts.  Loads run
+//     kAhead stages in front of the stores;
+//   * warp 1 copies each stage's atoms to TMEM (tcgen05.cp, in issue order with
+//     the products that read them) and issues four products (k = 64 each);
+//   * two accumulators let warps 2-5 store one tile while the next one runs.
+// Every wait is bounded as in situ_fused_gemm.cuh.
+
+namespace nvgemm {
+
+using fc1::decode_tile;
+using fc1::scan_experts;
+using fc1::smem_desc_sw128;
+using fc1::tc_fence_after;
+using fc1::tc_fence_before;
+using fc1::Tile;
+using fc1::tma_load_2d;
+using fc1::tmem_ld16;
+using fc1::tmem_ld_wait;
+using fc1::umma_commit;
+using fc1::wait_or_abort;
+
+constexpr int kBM = 128;
+constexpr int kStageK = 256;           // elements of k per stage
+constexpr int kStageRow = 128;         // their bytes
+constexpr int kSteps = 4;              // products (k = 64) per stage
+constexpr int kAtom = 512;             // bytes of scales of 128 rows and one step
+constexpr int kAhead = 4;              // stages of scales in registers
+constexpr int kMaxExperts = 1024;
+constexpr int kHeader = 256;
+
+// Sizes of a kernel with BN output columns per tile.
+template <int BN>
+struct Shape {
+  static constexpr int kScaleAtoms = (BN + 127) / 128;  // of B, per step
+  static constexpr int kScaleWarps = 1 + kScaleAtoms;
+  static constexpr int kThreads = 192 + 32 * kScaleWarps;
+  static constexpr int kABytes = kBM * kStageRow;
+  static constexpr int kBBytes = BN * kStageRow;
+  static constexpr int kScaleBytes = kSteps * kAtom * (1 + kScaleAtoms);
+  static constexpr int kStageBytes = kABytes + kBBytes + kScaleBytes;
+  static constexpr int kStages = (220 * 1024) / kStageBytes < 8 ? (220 * 1024) / kStageBytes : 8;
+  static constexpr int kScaleCols = kSteps * 4 * (1 + kScaleAtoms);  // TMEM columns of a stage's scales
+  // TMEM: two accumulators, then the scales of two stages
+  static constexpr int kScaleBase = 2 * BN;
+  static constexpr int kTmemCols = kScaleBase + 2 * kScaleCols <= 256 ? 256 : 512;
+  static_assert(kScaleBase + 2 * kScaleCols <= 512, "TMEM overflows");
+  static_assert(kBBytes % 1024 == 0 && kScaleBytes % 1024 == 0, "stages keep the 1024-byte alignment");
+  // kind::mxf4nvf4: E2M1 A and B (bits 7-9, 10-11 = 1), K-major, N >> 3 at bits
+  // 17-22, UE4M3 scales (bit 23 = 0), M >> 7 at bits 27-28, scale ids 0, k = 64.
+  static constexpr uint32_t kIdesc = (1u << 7) | (1u << 10) | (static_cast<uint32_t>(BN >> 3) << 17) | (1u << 27);
+};
+
+struct Args {
+  const uint8_t* a_scale;
+  int64_t a_scale_pitch;
+  const uint8_t* w_scale;
+  int64_t w_scale_pitch;
+  const float* a_amax;
+  const float* w_amax;
+  int64_t w_amax_stride;
+  const int64_t* offsets;
+  int experts;
+  int64_t tokens;
+  int k, n;
+  int a_vec, w_vec;  // the scales of a stage load as one 16-byte vector
+  char* out;
+  int64_t out_pitch;
+  int out_bf16;
+};
+
+// Descriptor of a 512-byte scale atom for tcgen05.cp.32x128b: no swizzle, rows
+// of 16 bytes, groups of 8 rows 128 bytes apart, descriptor version 1.
+__device__ __forceinline__ uint64_t atom_desc(uint32_t addr) {
+  return static_cast<uint64_t>((addr >> 4) & 0x3fffu) | (static_cast<uint64_t>(128 >> 4) << 32) |
+         (static_cast<uint64_t>(1) << 46);
+}
+__device__ __forceinline__ void scale_cp(uint32_t tmem, uint64_t desc) {
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
+}
+__device__ __forceinline__ void umma_nvfp4(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t sfa,
+                                           uint32_t sfb, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate));
+}
+
+// The 16 scales of one row and stage: `words` groups of four (64 elements of
+// k) exist, the others are zero.
+__device__ __forceinline__ uint4 load_scales(const uint8_t* p, int words, int vec) {
+  if (vec && words == 4) return __ldg(reinterpret_cast<const uint4*>(p));
+  const uint32_t* q = reinterpret_cast<const uint32_t*>(p);
+  uint4 r = make_uint4(0, 0, 0, 0);
+  if (words > 0) r.x = __ldg(q);
+  if (words > 1) r.y = __ldg(q + 1);
+  if (words > 2) r.z = __ldg(q + 2);
+  if (words > 3) r.w = __ldg(q + 3);
+  return r;
+}
+
+template <int BN>
+__global__ void __launch_bounds__(Shape<BN>::kThreads, 1)
+    situ_nvfp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_w,
+                           const Args a) {
+  using P = Shape<BN>;
+  extern __shared__ unsigned char smem_raw[];
+  const uint32_t raw_addr = smem_u32(smem_raw);
+  unsigned char* ring = smem_raw + ((1024u - (raw_addr & 1023u)) & 1023u);
+  unsigned char* header = ring + P::kStages * P::kStageBytes;
+  uint64_t* full = reinterpret_cast<uint64_t*>(header);
+  uint64_t* empty = full + P::kStages;
+  uint64_t* acc_full = empty + P::kStages;
+  uint64_t* acc_empty = acc_full + 2;
+  uint64_t* drain = acc_empty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  static_assert((2 * P::kStages + 5) * 8 + 8 <= kHeader, "header overflows");
+  int64_t* lo = reinterpret_cast<int64_t*>(header + kHeader);
+  int64_t* hi = lo + a.experts;
+  int* first_tile = reinterpret_cast<int*>(hi + a.experts);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int n_tiles = (a.n + BN - 1) / BN;
+  const int k_blocks = (a.k + kStageK - 1) / kStageK;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < P::kStages; ++s) {
+      mbar_init(&full[s], 1 + P::kScaleWarps);  // the TMA warp and each scale warp
+      mbar_init(&empty[s], 1);                  // the MMA warp's commit
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&acc_full[b], 1);
+      mbar_init(&acc_empty[b], 128);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    mbar_fence_init();
+  }
+  if (warp == 0) scan_experts<kBM>(a, n_tiles, lane, lo, hi, first_tile);
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                 "r"(P::kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  const int total = first_tile[a.experts];
+
+  if (warp == 0) {
+    // ---- codes ----
+    int stage = 0;
+    uint32_t phase = 0, issued = 0;
+    bool ok = true;
+    for (int t = blockIdx.x; ok && t < total; t += gridDim.x) {
+      const Tile tile = decode_tile<kBM>(t, first_tile, lo, hi, a.experts, n_tiles, BN);
+      const int32_t wrow = tile.expert * a.n + tile.n0;
+      for (int kb = 0; kb < k_blocks; ++kb) {
+        if (!wait_or_abort(&empty[stage], phase ^ 1u, abort_flag)) {
+          ok = false;
+          break;
+        }
+        if (lane == 0) {
+          unsigned char* st = ring + stage * P::kStageBytes;
+          mbar_arrive_expect_tx(&full[stage], P::kABytes + P::kBBytes);
+          tma_load_2d(st, &tmap_a, kb * kStageRow, static_cast<int32_t>(tile.m0), &full[stage]);
+          tma_load_2d(st + P::kABytes, &tmap_w, kb * kStageRow, wrow, &full[stage]);
+        }
+        __syncwarp();
+        issued |= 1u << stage;
+        if (++stage == P::kStages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+    if (!ok) {
+      // Aborted: let the copies this warp issued land (bounded) before the CTA exits.
+      for (int s = 0; s < P::kStages; ++s) {
+        if (!(issued & (1u << s))) continue;
+        const uint32_t ph = (s < stage) ? phase : (phase ^ 1u);
+        const unsigned long long t0 = global_timer_ns();
+        while (!mbar_try_wait(&full[s], ph) && global_timer_ns() - t0 < kWaitLimitNs) {
+        }
+      }
+    }
+  } else if (warp == 1) {
+    // ---- products ----
+    int stage = 0, it = 0, buf = 0;
+    uint32_t phase = 0, acc_phase = 0;
+    bool ok = true;
+    for (int t = blockIdx.x; ok && t < total; t += gridDim.x, ++it) {
+      const int b = it & 1;
+      if (!wait_or_abort(&acc_empty[b], ((acc_phase >> b) & 1u) ^ 1u, abort_flag)) break;
+      tc_fence_after();
+      const uint32_t d = tmem_base + static_cast<uint32_t>(b * BN);
+      for (int kb = 0; kb < k_blocks; ++kb) {
+        if (!wait_or_abort(&full[stage], phase, abort_flag)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        if (lane == 0) {
+          const uint32_t a_addr = smem_u32(ring + stage * P::kStageBytes), b_addr = a_addr + P::kABytes;
+          const uint32_t sc = b_addr + P::kBBytes;
+          const uint32_t sfa = tmem_base + P::kScaleBase + static_cast<uint32_t>(buf * P::kScaleCols);
+          const uint32_t sfb = sfa + kSteps * 4;
+#pragma unroll
+          for (int i = 0; i < kSteps * (1 + P::kScaleAtoms); ++i) scale_cp(sfa + 4 * i, atom_desc(sc + i * kAtom));
+#pragma unroll
+          for (int s = 0; s < kSteps; ++s)
+            umma_nvfp4(d, smem_desc_sw128(a_addr + s * 32), smem_desc_sw128(b_addr + s * 32), P::kIdesc, sfa + 4 * s,
+                       sfb + 4 * P::kScaleAtoms * s, (kb | s) != 0 ? 1u : 0u);
+          umma_commit(&empty[stage]);
+        }
+        __syncwarp();
+        buf ^= 1;
+        if (++stage == P::kStages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+      if (!ok) break;
+      if (lane == 0) umma_commit(&acc_full[b]);
+      __syncwarp();
+      acc_phase ^= 1u << b;
+    }
+    if (!ok || *abort_flag) {
+      if (lane == 0) umma_commit(drain);
+      __syncwarp();
+      const unsigned long long t0 = global_timer_ns();
+      while (!mbar_try_wait(drain, 0) && global_timer_ns() - t0 < kWaitLimitNs) {
+      }
+    }
+  } else if (warp < 6) {
+    // ---- epilogue: one accumulator row per thread ----
+    const int quarter = warp & 3;
+    const double unit_a = static_cast<double>(*a.a_amax) / 2688.0;
+    uint32_t acc_phase = 0;
+    int it = 0;
+    for (int t = blockIdx.x; t < total; t += gridDim.x, ++it) {
+      const int b = it & 1;
+      if (!wait_or_abort(&acc_full[b], (acc_phase >> b) & 1u, abort_flag)) break;
+      tc_fence_after();
+      const Tile tile = decode_tile<kBM>(t, first_tile, lo, hi, a.experts, n_tiles, BN);
+      const float alpha =
+          static_cast<float>(unit_a * (static_cast<double>(a.w_amax[tile.expert * a.w_amax_stride]) / 2688.0));
+      const int64_t row = tile.m0 + quarter * 32 + lane;
+      const bool valid = row < tile.m_end;
+      const int cols = min(BN, a.n - tile.n0);
+      const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(b * BN);
+      char* out = a.out + (valid ? row : 0) * a.out_pitch + static_cast<int64_t>(tile.n0) * (a.out_bf16 ? 2 : 4);
+#pragma unroll 1
+      for (int c = 0; c < cols; c += 16) {  // uniform over the warp
+        uint32_t r[16];
+        tmem_ld16(taddr + c, r);
+        tmem_ld_wait(r);
+        if (!valid) continue;
+        float v[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]) * alpha;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (c + 8 * h >= cols) continue;
+          const float* w = v + 8 * h;
+          if (a.out_bf16) {
+            *reinterpret_cast<uint4*>(out + (c + 8 * h) * 2) =
+                make_uint4(Bf16::pack(make_float2(w[0], w[1])), Bf16::pack(make_float2(w[2], w[3])),
+                           Bf16::pack(make_float2(w[4], w[5])), Bf16::pack(make_float2(w[6], w[7])));
+          } else {
+            float4* o = reinterpret_cast<float4*>(out + (c + 8 * h) * 4);
+            o[0] = make_float4(w[0], w[1], w[2], w[3]);
+            o[1] = make_float4(w[4], w[5], w[6], w[7]);
+          }
+        }
+      }
+      tc_fence_before();
+      mbar_arrive(&acc_empty[b]);
+      acc_phase ^= 1u << b;
+    }
+  } else {
+    // ---- block scales: warp 6 the rows of A, warp 7 + j rows [128 j, 128 j + 128) of B ----
+    const int part = warp - 6;
+    const bool is_a = part == 0;
+    const uint8_t* base = is_a ? a.a_scale : a.w_scale;
+    const int64_t pitch = is_a ? a.a_scale_pitch : a.w_scale_pitch;
+    const int vec = is_a ? a.a_vec : a.w_vec;
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int t = blockIdx.x; ok && t < total; t += gridDim.x) {
+      const Tile tile = decode_tile<kBM>(t, first_tile, lo, hi, a.experts, n_tiles, BN);
+      // first row of this warp's 128 and how many of them exist
+      const int64_t row0 = is_a ? tile.m0 : static_cast<int64_t>(tile.expert) * a.n + tile.n0 + (part - 1) * 128;
+      const int64_t left = is_a ? tile.m_end - tile.m0 : min(a.n - tile.n0, BN) - (part - 1) * 128;
+      const uint8_t* rows[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) rows[j] = lane + 32 * j < left ? base + (row0 + lane + 32 * j) * pitch : nullptr;
+      uint4 v[kAhead][4];
+      auto fetch = [&](uint4 (&w)[4], int kb) {
+        const int words = min(4, (a.k - kb * kStageK) / 64);  // <= 0 past the end
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          w[j] = rows[j] != nullptr ? load_scales(rows[j] + kb * 16, words, vec) : make_uint4(0, 0, 0, 0);
+      };
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) fetch(v[u], u);
+      for (int kb0 = 0; ok && kb0 < k_blocks; kb0 += kAhead) {
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+          if (kb0 + u >= k_blocks) break;
+          if (!wait_or_abort(&empty[stage], phase ^ 1u, abort_flag)) {
+            ok = false;
+            break;
+          }
+          // atom of step s: word s of rows l, l + 32, l + 64, l + 96
+          unsigned char* st = ring + stage * P::kStageBytes + P::kABytes + P::kBBytes + lane * 16 +
+                              (is_a ? 0 : kSteps * kAtom + (part - 1) * kAtom);
+          const int apart = is_a ? kAtom : P::kScaleAtoms * kAtom;
+          const uint4(&w)[4] = v[u];
+          *reinterpret_cast<uint4*>(st) = make_uint4(w[0].x, w[1].x, w[2].x, w[3].x);
+          *reinterpret_cast<uint4*>(st + apart) = make_uint4(w[0].y, w[1].y, w[2].y, w[3].y);
+          *reinterpret_cast<uint4*>(st + 2 * apart) = make_uint4(w[0].z, w[1].z, w[2].z, w[3].z);
+          *reinterpret_cast<uint4*>(st + 3 * apart) = make_uint4(w[0].w, w[1].w, w[2].w, w[3].w);
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the copies to TMEM read them
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&full[stage]);
+          fetch(v[u], kb0 + u + kAhead);
+          if (++stage == P::kStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(P::kTmemCols) : "memory");
+}
+
+// ---- host ---------------------------------------------------------------------
+
+// 2-D byte tensor map of packed codes [rows, >= inner bytes], boxes of 128
+// bytes x `box_rows` with the 128-byte swizzle.
+situ_status_t code_map(CUtensorMap* m, const void* base, int64_t inner, int64_t rows, int64_t pitch, int box_rows) {
+  EncodeTiledFn fn = encode_tiled();
+  if (fn == nullptr) return fail(SITU_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(pitch)};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(kStageRow), static_cast<cuuint32_t>(box_rows)};
+  const cuuint32_t estr[2] = {1, 1};
+  const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(SITU_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", static_cast<int>(r));
+  return SITU_OK;
+}
+
+template <int BN>
+situ_status_t launch(const void* a_data, int64_t a_pitch, const void* w_data, int64_t w_pitch, const Args& a,
+                     cudaStream_t s) {
+  using P = Shape<BN>;
+  CUtensorMap ma, mw;
+  situ_status_t st = code_map(&ma, a_data, a.k / 2, a.tokens, a_pitch, kBM);
+  if (st != SITU_OK) return st;
+  st = code_map(&mw, w_data, a.k / 2, static_cast<int64_t>(a.experts) * a.n, w_pitch, BN);
+  if (st != SITU_OK) return st;
+  int grid = 0;
+  st = device_sm_count(&grid);
+  if (st != SITU_OK) return st;
+  const int cap = g_max_ctas.load(std::memory_order_relaxed);
+  if (cap > 0 && grid > cap) grid = cap;
+  // no more CTAs than tiles there can be: every expert may end in a part of one
+  const int64_t most = ((a.tokens + kBM - 1) / kBM + a.experts - 1) * ((a.n + BN - 1) / BN);
+  if (grid > most) grid = static_cast<int>(most);
+  const int smem = 1024 + P::kStages * P::kStageBytes + kHeader + a.experts * 20 + 8;
+  st = ensure_smem(reinterpret_cast<const void*>(situ_nvfp4_gemm_kernel<BN>), smem);
+  if (st != SITU_OK) return st;
+  situ_nvfp4_gemm_kernel<BN><<<grid, P::kThreads, smem, s>>>(ma, mw, a);
+  return check_launch("situ_glu_nvfp4_gemm");
+}
+
+}  // namespace nvgemm
+
+// Checks of a stored matrix' codes and scales (row pitches in bytes).
+situ_status_t check_codes(const void* data, int64_t data_pitch, const void* scale, int64_t scale_pitch, int64_t rows,
+                          int64_t cols, int data_align, int scale_align, const char* name) {
+  if (data == nullptr || scale == nullptr) return fail(SITU_ERR_INVALID_ARG, "%s codes or scales are NULL", name);
+  if (!span_fits(rows, data_pitch, cols / 2, 1) || !span_fits(rows, scale_pitch, cols / 16, 1))
+    return fail(SITU_ERR_INVALID_ARG, "extent of %s overflows int64", name);
+  if (!aligned(data, data_align) || data_pitch % data_align != 0 || !aligned(scale, scale_align) ||
+      scale_pitch % scale_align != 0)
+    return fail(SITU_ERR_MISALIGNED, "%s codes (%d bytes) or scales (%d) base or row pitch misaligned", name, data_align,
+                scale_align);
+  return SITU_OK;
+}
+
+Span bytes_span(const void* p, size_t n) {
+  const uintptr_t b = reinterpret_cast<uintptr_t>(p);
+  return {b, b + n};
+}
+
+// Size checks shared by quantise and dequantise.
+situ_status_t store_check(situ_dtype_t dtype, int64_t rows, int64_t cols, int64_t stride) {
+  if (!valid_dtype(dtype)) return fail(SITU_ERR_INVALID_ARG, "dtype %d is not a situ_dtype_t", (int)dtype);
+  if (rows < 0) return fail(SITU_ERR_INVALID_ARG, "rows = %lld < 0", (long long)rows);
+  if (cols <= 0 || cols % 16 != 0)
+    return fail(SITU_ERR_INVALID_ARG, "cols must be a positive multiple of 16, got %lld", (long long)cols);
+  if (cols > (int64_t(1) << 31)) return fail(SITU_ERR_UNSUPPORTED, "cols = %lld exceeds 2^31", (long long)cols);
+  if (stride < cols) return fail(SITU_ERR_INVALID_ARG, "a row stride is shorter than its row");
+  return SITU_OK;
+}
+
+void fill_store(StoreArgs* a, int64_t rows, int64_t cols) {
+  a->rows = rows;
+  a->per_row = static_cast<uint32_t>(cols / 16);
+  a->blocks = rows * (cols / 16);
+}
+
+// Rows without a gap between them are one long row to the kernels' loops.
+int wide_rows(const void* p, int64_t pitch) { return aligned(p, 32) && pitch % 32 == 0; }
+
+}  // namespace
+
+int nvfp4_device_status(int clear) {
+  int v = 0;
+  if (cudaMemcpyFromSymbol(&v, g_device_status, sizeof v) != cudaSuccess) return -1;
+  if (clear && v != 0) {
+    const int zero = 0;
+    if (cudaMemcpyToSymbol(g_device_status, &zero, sizeof zero) != cudaSuccess) return -1;
+  }
+  return v;
+}
+
+extern "C" {
+
+situ_status_t situ_glu_nvfp4_quantize(const void* x, situ_dtype_t dtype, int64_t rows, int64_t cols,
+                                      int64_t x_row_stride, void* data, int64_t data_row_stride, void* scale,
+                                      int64_t scale_row_stride, float* amax, int amax_given, void* stream) {
+  tl_last_error[0] = '\0';
+  situ_status_t st = store_check(dtype, rows, cols, x_row_stride);
+  if (st != SITU_OK) return st;
+  if (amax_given < 0 || amax_given > 2) return fail(SITU_ERR_INVALID_ARG, "amax_given must be 0, 1 or 2");
+  const bool only = amax_given == 2;
+  if (!only && (data_row_stride < cols / 2 || scale_row_stride < cols / 16))
+    return fail(SITU_ERR_INVALID_ARG, "NVFP4 data or scale row pitch shorter than a row");
+  if (amax == nullptr) return fail(SITU_ERR_INVALID_ARG, "amax is NULL");
+  if (!aligned(amax, 4)) return fail(SITU_ERR_MISALIGNED, "amax not 4-byte aligned");
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const int es = elem_size(dtype);
+  if (rows > 0) {
+    if (x == nullptr) return fail(SITU_ERR_INVALID_ARG, "x is NULL");
+    if (!span_fits(rows, x_row_stride, cols, es)) return fail(SITU_ERR_INVALID_ARG, "extent of x overflows int64");
+    if (!aligned(x, 16) || (x_row_stride * es) % 16 != 0)
+      return fail(SITU_ERR_MISALIGNED, "x base or row pitch not 16-byte aligned");
+    if (!only) {
+      st = check_codes(data, data_row_stride, scale, scale_row_stride, rows, cols, 8, 1, "NVFP4");
+      if (st != SITU_OK) return st;
+    }
+    const Span in = matrix_span(x, rows, x_row_stride, cols, es);
+    const Span outs[] = {bytes_span(amax, 4), only ? Span{0, 0} : matrix_span(data, rows, data_row_stride, cols / 2, 1),
+                         only ? Span{0, 0} : matrix_span(scale, rows, scale_row_stride, cols / 16, 1)};
+    for (int i = 0; i < 3; ++i) {
+      if (overlap(outs[i], in)) return fail(SITU_ERR_INVALID_ARG, "an output overlaps x");
+      for (int k = i + 1; k < 3; ++k)
+        if (overlap(outs[i], outs[k])) return fail(SITU_ERR_INVALID_ARG, "outputs overlap each other");
+    }
+  }
+  if (amax_given != 1) {
+    cudaError_t err = cudaMemsetAsync(amax, 0, sizeof(float), s);
+    if (err != cudaSuccess) return fail(SITU_ERR_CUDA, "cudaMemsetAsync: %s", cudaGetErrorString(err));
+  }
+  if (rows == 0) return SITU_OK;
+  StoreArgs a{};
+  a.x = static_cast<const char*>(x);
+  a.x_pitch = x_row_stride * es;
+  a.data = static_cast<char*>(data);
+  a.data_pitch = data_row_stride;
+  a.scale = static_cast<uint8_t*>(scale);
+  a.scale_pitch = scale_row_stride;
+  a.amax = amax;
+  a.amax_out = reinterpret_cast<unsigned int*>(amax);
+  a.wide = wide_rows(x, a.x_pitch);
+  fill_store(&a, rows, cols);
+  const bool bf = dtype == SITU_DTYPE_BF16;
+  const int64_t ctas = (a.blocks + kStoreThreads - 1) / kStoreThreads;
+  int grid = 0;
+  if (amax_given != 1) {
+    auto k = bf ? situ_nvfp4_amax_kernel<Bf16> : situ_nvfp4_amax_kernel<F32>;
+    st = launch_grid(reinterpret_cast<const void*>(k), kStoreThreads, 0, ctas, &grid);
+    if (st != SITU_OK) return st;
+    k<<<grid, kStoreThreads, 0, s>>>(a);
+    st = check_launch("situ_glu_nvfp4_quantize (amax)");
+    if (st != SITU_OK || only) return st;
+  }
+  auto k = bf ? situ_nvfp4_quantize_kernel<Bf16> : situ_nvfp4_quantize_kernel<F32>;
+  st = launch_grid(reinterpret_cast<const void*>(k), kStoreThreads, 0, ctas, &grid);
+  if (st != SITU_OK) return st;
+  k<<<grid, kStoreThreads, 0, s>>>(a);
+  return check_launch("situ_glu_nvfp4_quantize");
+}
+
+situ_status_t situ_glu_nvfp4_dequantize(const void* data, int64_t data_row_stride, const void* scale,
+                                        int64_t scale_row_stride, const float* amax, int64_t rows, int64_t cols,
+                                        void* out, situ_dtype_t dtype, int64_t out_row_stride, void* stream) {
+  tl_last_error[0] = '\0';
+  situ_status_t st = store_check(dtype, rows, cols, out_row_stride);
+  if (st != SITU_OK) return st;
+  if (data_row_stride < cols / 2 || scale_row_stride < cols / 16)
+    return fail(SITU_ERR_INVALID_ARG, "NVFP4 data or scale row pitch shorter than a row");
+  if (rows == 0) return SITU_OK;
+  if (amax == nullptr || out == nullptr) return fail(SITU_ERR_INVALID_ARG, "amax or out is NULL");
+  if (!aligned(amax, 4)) return fail(SITU_ERR_MISALIGNED, "amax not 4-byte aligned");
+  const int es = elem_size(dtype);
+  st = check_codes(data, data_row_stride, scale, scale_row_stride, rows, cols, 8, 1, "NVFP4");
+  if (st != SITU_OK) return st;
+  if (!span_fits(rows, out_row_stride, cols, es)) return fail(SITU_ERR_INVALID_ARG, "extent of out overflows int64");
+  if (!aligned(out, 16) || (out_row_stride * es) % 16 != 0)
+    return fail(SITU_ERR_MISALIGNED, "out base or row pitch not 16-byte aligned");
+  const Span o = matrix_span(out, rows, out_row_stride, cols, es);
+  if (overlap(o, matrix_span(data, rows, data_row_stride, cols / 2, 1)) ||
+      overlap(o, matrix_span(scale, rows, scale_row_stride, cols / 16, 1)) || overlap(o, bytes_span(amax, 4)))
+    return fail(SITU_ERR_INVALID_ARG, "out overlaps an input");
+  StoreArgs a{};
+  a.data = const_cast<char*>(static_cast<const char*>(data));
+  a.data_pitch = data_row_stride;
+  a.scale = const_cast<uint8_t*>(static_cast<const uint8_t*>(scale));
+  a.scale_pitch = scale_row_stride;
+  a.amax = amax;
+  a.out = static_cast<char*>(out);
+  a.out_pitch = out_row_stride * es;
+  a.wide = wide_rows(out, a.out_pitch);
+  fill_store(&a, rows, cols);
+  auto k = dtype == SITU_DTYPE_BF16 ? situ_nvfp4_dequantize_kernel<Bf16> : situ_nvfp4_dequantize_kernel<F32>;
+  int grid = 0;
+  st = launch_grid(reinterpret_cast<const void*>(k), kStoreThreads, 0, (a.blocks + kStoreThreads - 1) / kStoreThreads,
+                   &grid);
+  if (st != SITU_OK) return st;
+  k<<<grid, kStoreThreads, 0, static_cast<cudaStream_t>(stream)>>>(a);
+  return check_launch("situ_glu_nvfp4_dequantize");
+}
+
+situ_status_t situ_glu_nvfp4_gemm(const void* a_data, int64_t a_data_row_stride, const void* a_scale,
+                                  int64_t a_scale_row_stride, const float* a_amax, int64_t tokens, int64_t k,
+                                  const void* w_data, int64_t w_data_row_stride, const void* w_scale,
+                                  int64_t w_scale_row_stride, const float* w_amax, int64_t w_amax_stride,
+                                  int64_t experts, int64_t n, const int64_t* offsets, void* out,
+                                  situ_dtype_t out_dtype, int64_t out_row_stride, void* stream) {
+  tl_last_error[0] = '\0';
+  if (!valid_dtype(out_dtype)) return fail(SITU_ERR_INVALID_ARG, "out_dtype %d is not a situ_dtype_t", (int)out_dtype);
+  if (tokens < 0) return fail(SITU_ERR_INVALID_ARG, "tokens = %lld < 0", (long long)tokens);
+  if (k < 64 || k % 64 != 0)
+    return fail(SITU_ERR_UNSUPPORTED, "k must be a positive multiple of 64, got %lld", (long long)k);
+  if (n < 8 || n % 8 != 0)
+    return fail(SITU_ERR_UNSUPPORTED, "n must be a positive multiple of 8, got %lld", (long long)n);
+  if (experts < 1 || experts > nvgemm::kMaxExperts)
+    return fail(SITU_ERR_UNSUPPORTED, "experts must be in [1, %d], got %lld", nvgemm::kMaxExperts, (long long)experts);
+  if (tokens > INT32_MAX - 256 || n > INT32_MAX / experts - 256 || k > INT32_MAX - 256)
+    return fail(SITU_ERR_UNSUPPORTED, "sizes exceed the 32-bit tensor-map coordinates");
+  // tiles are numbered in 32 bits (the narrowest have 64 columns)
+  if ((tokens / nvgemm::kBM + experts + 1) > INT32_MAX / (n / 64 + 1))
+    return fail(SITU_ERR_UNSUPPORTED, "too many output tiles");
+  if (offsets == nullptr && experts != 1) return fail(SITU_ERR_INVALID_ARG, "offsets is NULL with %lld experts", (long long)experts);
+  if (a_data_row_stride < k / 2 || a_scale_row_stride < k / 16 || w_data_row_stride < k / 2 ||
+      w_scale_row_stride < k / 16 || out_row_stride < n)
+    return fail(SITU_ERR_INVALID_ARG, "a row stride is shorter than its row");
+  if (w_amax_stride < 0) return fail(SITU_ERR_INVALID_ARG, "w_amax_stride < 0");
+  if (tokens == 0) return SITU_OK;
+  if (a_amax == nullptr || w_amax == nullptr || out == nullptr)
+    return fail(SITU_ERR_INVALID_ARG, "a_amax, w_amax or out is NULL");
+  if (!aligned(a_amax, 4) || !aligned(w_amax, 4) || (offsets != nullptr && !aligned(offsets, 8)))
+    return fail(SITU_ERR_MISALIGNED, "a_amax, w_amax (4 bytes) or offsets (8) misaligned");
+  situ_status_t st = check_codes(a_data, a_data_row_stride, a_scale, a_scale_row_stride, tokens, k, 16, 4, "a");
+  if (st != SITU_OK) return st;
+  st = check_codes(w_data, w_data_row_stride, w_scale, w_scale_row_stride, experts * n, k, 16, 4, "w");
+  if (st != SITU_OK) return st;
+  const int oes = elem_size(out_dtype);
+  if (!span_fits(tokens, out_row_stride, n, oes) || !span_fits(experts, w_amax_stride, 1, 4))
+    return fail(SITU_ERR_INVALID_ARG, "tensor extent overflows int64");
+  if (!aligned(out, 16) || (out_row_stride * oes) % 16 != 0)
+    return fail(SITU_ERR_MISALIGNED, "out base or row pitch not 16-byte aligned");
+  const Span o = matrix_span(out, tokens, out_row_stride, n, oes);
+  if (overlap(o, matrix_span(a_data, tokens, a_data_row_stride, k / 2, 1)) ||
+      overlap(o, matrix_span(a_scale, tokens, a_scale_row_stride, k / 16, 1)) ||
+      overlap(o, matrix_span(w_data, experts * n, w_data_row_stride, k / 2, 1)) ||
+      overlap(o, matrix_span(w_scale, experts * n, w_scale_row_stride, k / 16, 1)) ||
+      overlap(o, bytes_span(a_amax, 4)) || overlap(o, matrix_span(w_amax, experts, w_amax_stride, 1, 4)) ||
+      (offsets != nullptr && overlap(o, bytes_span(offsets, static_cast<size_t>(experts + 1) * 8))))
+    return fail(SITU_ERR_INVALID_ARG, "out overlaps an input");
+
+  nvgemm::Args a{};
+  a.a_scale = static_cast<const uint8_t*>(a_scale);
+  a.a_scale_pitch = a_scale_row_stride;
+  a.w_scale = static_cast<const uint8_t*>(w_scale);
+  a.w_scale_pitch = w_scale_row_stride;
+  a.a_amax = a_amax;
+  a.w_amax = w_amax;
+  a.w_amax_stride = w_amax_stride;
+  a.offsets = offsets;
+  a.experts = static_cast<int>(experts);
+  a.tokens = tokens;
+  a.k = static_cast<int>(k);
+  a.n = static_cast<int>(n);
+  a.a_vec = aligned(a_scale, 16) && a_scale_row_stride % 16 == 0;
+  a.w_vec = aligned(w_scale, 16) && w_scale_row_stride % 16 == 0;
+  a.out = static_cast<char*>(out);
+  a.out_pitch = out_row_stride * oes;
+  a.out_bf16 = out_dtype == SITU_DTYPE_BF16;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  int sms = 0;
+  st = device_sm_count(&sms);
+  if (st != SITU_OK) return st;
+  // Narrow tiles where wide ones would leave SMs idle (few rows: the weights'
+  // bandwidth is the bound, and more SMs draw more of it).
+  const int64_t wide = ((tokens + nvgemm::kBM - 1) / nvgemm::kBM) * ((n + 191) / 192);
+  if (wide < sms) return nvgemm::launch<64>(a_data, a_data_row_stride, w_data, w_data_row_stride, a, s);
+  return nvgemm::launch<192>(a_data, a_data_row_stride, w_data, w_data_row_stride, a, s);
+}
+
+}  // extern "C"

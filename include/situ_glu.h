@@ -401,6 +401,185 @@ situ_status_t situ_attn_res_fwd(const void *blocks, int64_t nblocks, int64_t blo
                                 void *out, situ_dtype_t out_dtype, int64_t out_row_stride,
                                 void *stream);
 
+/* ---- Residual addition + RMS norm ---------------------------------------------
+ * The norm in front of the router and the experts, on the attention-residual
+ * core's conventions (RMSNorm in its standard form, NeMo AutoModel API
+ * kimi_k3.situ `_attn_res_core`).  Per row t:
+ *   h[t, :] = x[t, :] + residual[t, :]   rounded to `dtype`  (h = x without a residual)
+ *   y[t, i] = h[t, i] / sqrt(mean_i h[t, i]^2 + epsilon) * weight[i]
+ * The norm is that of the row as it is held (after the rounding), so the
+ * backward, which reads h, differentiates exactly what the forward computed.
+ *
+ *   x                 [tokens, >= hidden] in dtype, row pitch x_row_stride
+ *   residual          [tokens, >= hidden] in dtype, row pitch residual_row_stride;
+ *                     NULL: none, and h must be NULL too
+ *   weight            [hidden] in weight_dtype, aligned to
+ *                     min(16, 16 / sizeof(dtype) * sizeof(weight_dtype)) bytes
+ *   epsilon           finite and >= 0
+ *   h                 [tokens, >= hidden] in dtype, written
+ *   y                 [tokens, >= hidden] in dtype, written
+ * Outputs must not overlap an input or each other.  tokens == 0 launches
+ * nothing.  hidden * sizeof(dtype) <= 65536 (SITU_ERR_UNSUPPORTED otherwise)
+ * and a multiple of 16, matrices 16-byte aligned with row pitches of a multiple
+ * of 16 bytes (SITU_ERR_MISALIGNED).  A row holding a NaN or an
+ * infinity has NaNs in y; other rows are not affected.  Results do not depend
+ * on the launch size. */
+situ_status_t situ_glu_rms_norm_fwd(const void *x, situ_dtype_t dtype, int64_t tokens, int64_t hidden,
+                                    int64_t x_row_stride,
+                                    const void *residual, int64_t residual_row_stride,
+                                    const void *weight, situ_dtype_t weight_dtype, double epsilon,
+                                    void *h, int64_t h_row_stride,
+                                    void *y, int64_t y_row_stride,
+                                    void *stream);
+
+/* As situ_glu_rms_norm_fwd with y as MXFP8 (layout, rules and restrictions of
+ * situ_glu_fwd_mxfp8: E4M3 codes y_data [tokens, >= hidden], a scale byte per
+ * 32 columns y_scale [tokens, >= hidden / 32], row pitches in bytes; hidden a
+ * multiple of 32), quantised from the fp32 values. */
+situ_status_t situ_glu_rms_norm_fwd_mxfp8(const void *x, situ_dtype_t dtype, int64_t tokens, int64_t hidden,
+                                          int64_t x_row_stride,
+                                          const void *residual, int64_t residual_row_stride,
+                                          const void *weight, situ_dtype_t weight_dtype, double epsilon,
+                                          void *h, int64_t h_row_stride,
+                                          void *y_data, int64_t y_data_row_stride,
+                                          void *y_scale, int64_t y_scale_row_stride,
+                                          situ_mx_rule_t rule, void *stream);
+
+/* Backward.  With q[t] = 1 / sqrt(mean_i h[t, i]^2 + epsilon), recomputed from h:
+ *   d_x[t, i]   = grad_h[t, i] + q g[t, i] - h[t, i] q^3 mean_j g[t, j] h[t, j],   g = grad_y weight
+ *   d_weight[i] = sum_t grad_y[t, i] h[t, i] q[t]
+ * d_x is the gradient of both x and residual.
+ *
+ *   grad_y, h         [tokens, >= hidden] in dtype (h: the forward's h, or x
+ *                     where there was no residual)
+ *   grad_h            the gradient that reaches h itself, [tokens, >= hidden] in
+ *                     dtype, or NULL (zero)
+ *   d_x               [tokens, >= hidden] in dtype, written
+ *   d_weight          [hidden] in weight_dtype, aligned to its element; NULL: not
+ *                     wanted.  Summed in fp32 in an order fixed by the shape (zero
+ *                     when tokens == 0).
+ *   workspace         >= situ_glu_rms_norm_bwd_workspace_bytes() bytes, 16-byte
+ *                     aligned; may be NULL when that is 0
+ * Other rules as for situ_glu_rms_norm_fwd. */
+situ_status_t situ_glu_rms_norm_bwd(const void *grad_y, int64_t grad_y_row_stride,
+                                    const void *grad_h, int64_t grad_h_row_stride,
+                                    const void *h, situ_dtype_t dtype, int64_t tokens, int64_t hidden,
+                                    int64_t h_row_stride,
+                                    const void *weight, situ_dtype_t weight_dtype, double epsilon,
+                                    void *d_x, int64_t d_x_row_stride,
+                                    void *d_weight,
+                                    void *workspace, size_t workspace_bytes, void *stream);
+
+/* Bytes of workspace situ_glu_rms_norm_bwd needs: one fp32 row of partial sums
+ * per chunk of rows (at most 296 chunks) when want_dweight != 0, else 0. */
+size_t situ_glu_rms_norm_bwd_workspace_bytes(int64_t tokens, int64_t hidden, int want_dweight);
+
+/* ---- Expert layer for a few tokens ----------------------------------------------
+ * The whole routed feed-forward layer of a decoding step, in two kernels.  With
+ * W1_e = w1[e] ([2 inter, hidden]: inter gate rows, then inter up rows) and
+ * W2_e = w2[e] ([hidden, inter]),
+ *   G, U   = W1_e x[t]                                    (fp32 sums)
+ *   a[t,e] = T_g(G) T_u(U) w[t, e]                        (as situ_glu_fwd, in fp32)
+ *   y[t]   = sum over the experts e of token t of W2_e a[t, e]
+ * Each expert's weights are read once, whatever the number of its tokens.
+ * a enters the second product as a pair of bf16 numbers (its rounding and the
+ * remainder's), which keeps 16 bits of its significand.
+ *
+ *   x                 bf16 [tokens, >= hidden], row pitch x_row_stride
+ *   topk_ids          DEVICE int64 [tokens, >= topk], row pitch topk_ids_row_stride: the
+ *                     experts of each token.  An id outside [0, experts) is skipped (an
+ *                     empty slot of a padded batch: -1); an id that a token names more
+ *                     than once counts with the sum of its weights.
+ *   topk_weights      [tokens, >= topk] in weights_dtype, row pitch
+ *                     topk_weights_row_stride; NULL: 1
+ *   w1                bf16 [experts * 2 inter, >= hidden], row pitch w1_row_stride
+ *   w2                bf16 [experts * hidden, >= inter], row pitch w2_row_stride
+ *   y                 bf16 [tokens, >= hidden], row pitch y_row_stride; a token without
+ *                     an expert gets zeros.  Must not overlap an input.
+ *   workspace         >= situ_glu_moe_workspace_bytes() bytes, 16-byte aligned, contents
+ *                     ignored on entry and undefined on exit.  Calls that overlap on the
+ *                     GPU need a workspace each.
+ * tokens <= 64, topk in [1, 16], experts in [1, 1024], hidden and inter multiples
+ * of 64 up to 32768 (SITU_ERR_UNSUPPORTED otherwise: for more tokens group the rows
+ * and call situ_glu_fc1_fwd); x, w1, w2, y 16-byte aligned with row pitches of a
+ * multiple of 16 bytes.  tokens == 0 launches nothing.  Results do not depend on
+ * the launch size, nor a token's on the other tokens of the call beyond the
+ * rounding of its sums. */
+situ_status_t situ_glu_moe_fwd(const void *x, int64_t tokens, int64_t hidden, int64_t x_row_stride,
+                               const int64_t *topk_ids, int64_t topk, int64_t topk_ids_row_stride,
+                               const void *topk_weights, situ_dtype_t weights_dtype,
+                               int64_t topk_weights_row_stride,
+                               const void *w1, int64_t experts, int64_t inter, int64_t w1_row_stride,
+                               const void *w2, int64_t w2_row_stride,
+                               double beta, int has_linear_beta, double linear_beta,
+                               void *y, int64_t y_row_stride,
+                               void *workspace, size_t workspace_bytes, void *stream);
+
+/* Bytes of workspace situ_glu_moe_fwd needs: per (token, choice) the activations
+ * as two bf16 rows of inter and an fp32 row of hidden, and a counter per 16
+ * columns of y, each rounded up to 256. */
+size_t situ_glu_moe_workspace_bytes(int64_t tokens, int64_t topk, int64_t hidden, int64_t inter);
+
+/* ---- NVFP4 storage and product ----------------------------------------------------
+ * Quantisation of any matrix to the format of situ_glu_fwd_nvfp4 (the weights of
+ * an NVFP4 product, or the rows that enter it): with A the largest finite |x|,
+ *   scale  [rows, >= cols / 16]: s_b = E4M3(amax_b * 448 / A), 0x7F for a block
+ *          holding NaN or infinity (whose codes are 0)
+ *   data   [rows, >= cols / 2]: packed E2M1 codes of x * 2688 / (A s_b)
+ * with S_enc = 2688 / A = 1 when A is 0 or not finite.  Every code and scale is
+ * the correctly rounded one (nearest, ties to even, of the exact quotient of the
+ * stored numbers), saturating where a given A is below the matrix' own.
+ *   x                 [rows, >= cols] in dtype, row pitch x_row_stride elements
+ *   data, scale       row pitches in BYTES; data 8-byte aligned with a pitch of a
+ *                     multiple of 8
+ *   amax, amax_given  DEVICE fp32, as for situ_glu_fwd_nvfp4 (0: computed and
+ *                     written; 1: given; 2: only computed, data and scale may be NULL)
+ * cols a multiple of 16; x 16-byte aligned with a row pitch of a multiple of 16
+ * bytes.  Outputs must not overlap x or each other.  rows == 0: A = 0. */
+situ_status_t situ_glu_nvfp4_quantize(const void *x, situ_dtype_t dtype, int64_t rows, int64_t cols,
+                                      int64_t x_row_stride,
+                                      void *data, int64_t data_row_stride,
+                                      void *scale, int64_t scale_row_stride,
+                                      float *amax, int amax_given, void *stream);
+
+/* The way back: out[r, i] = q s_b A / 2688 in dtype (fp32 products, one rounding;
+ * NaN for a block whose scale is 0x7F).  out 16-byte aligned with a row pitch of a
+ * multiple of 16 bytes; data as above. */
+situ_status_t situ_glu_nvfp4_dequantize(const void *data, int64_t data_row_stride,
+                                        const void *scale, int64_t scale_row_stride,
+                                        const float *amax, int64_t rows, int64_t cols,
+                                        void *out, situ_dtype_t dtype, int64_t out_row_stride, void *stream);
+
+/* Grouped NVFP4 product on the fp4 tensor cores: for row r of expert e (rows
+ * [offsets[e], offsets[e + 1]) of a),
+ *   out[r, n] = sum_k a[r, k] w[e N + n, k]
+ * over the values a and w stand for (as situ_glu_nvfp4_dequantize; the block
+ * scales enter the tensor cores, A_a A_w / 2688^2 the epilogue), fp32 sums, one
+ * rounding to out_dtype.
+ *   a_data, a_scale, a_amax   rows [tokens, k] in NVFP4 (situ_glu_nvfp4_quantize or
+ *                             situ_glu_fwd_nvfp4); row pitches in bytes; a_amax one
+ *                             DEVICE fp32
+ *   w_data, w_scale           [experts * n, k] in NVFP4; row pitches in bytes
+ *   w_amax                    DEVICE fp32, expert e's at w_amax[e * w_amax_stride]
+ *                             (0: one for all)
+ *   offsets                   DEVICE int64 [experts + 1] as for situ_glu_fc1_fwd, or
+ *                             NULL with experts == 1: every row
+ *   out                       [tokens, >= n] in out_dtype, row pitch out_row_stride
+ *                             elements.  Rows outside every expert are not written.
+ * k a multiple of 64, n of 8, experts in [1, 1024] (SITU_ERR_UNSUPPORTED otherwise);
+ * data 16-byte aligned with pitches of a multiple of 16, scales 4-byte aligned with
+ * pitches of a multiple of 4, out 16-byte aligned with a row pitch of a multiple of
+ * 16 bytes.  A scale of 0x7F (NaN) makes its output rows or columns NaN.  tokens == 0
+ * launches nothing.  Every internal wait is bounded (situ_glu_device_status). */
+situ_status_t situ_glu_nvfp4_gemm(const void *a_data, int64_t a_data_row_stride,
+                                  const void *a_scale, int64_t a_scale_row_stride, const float *a_amax,
+                                  int64_t tokens, int64_t k,
+                                  const void *w_data, int64_t w_data_row_stride,
+                                  const void *w_scale, int64_t w_scale_row_stride,
+                                  const float *w_amax, int64_t w_amax_stride,
+                                  int64_t experts, int64_t n, const int64_t *offsets,
+                                  void *out, situ_dtype_t out_dtype, int64_t out_row_stride, void *stream);
+
 /* Static, human-readable name of a status code. */
 const char *situ_glu_status_string(situ_status_t status);
 
