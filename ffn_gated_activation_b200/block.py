@@ -9,6 +9,7 @@ allocates belongs to that stream.
 """
 from __future__ import annotations
 
+import contextlib
 import math
 
 import torch
@@ -20,28 +21,33 @@ from .functional import (DEFAULT_BETA, DEFAULT_LINEAR_BETA, _check_beta, _dtype_
 DEFAULT_EPSILON = 1e-6
 
 
+_current_device = torch._C._cuda_getDevice
+_current_stream = torch._C._cuda_getCurrentRawStream  # (device index) -> cudaStream_t
+
+
 class _Scope:
     """The device (and, if given, the stream) a call runs on; yields the stream's handle."""
 
     __slots__ = ("device", "stream", "entered")
 
     def __init__(self, device, stream):
-        self.device, self.stream, self.entered = device, stream, []
+        self.device, self.stream, self.entered = device, stream, None
 
     def __enter__(self) -> int:
-        if self.stream is not None and self.stream.device != self.device:
-            raise ValueError(f"stream is on {self.stream.device}, the tensors on {self.device}")
-        if self.device.index != torch.cuda.current_device():
-            self.entered.append(torch.cuda.device(self.device))
-        if self.stream is not None:
-            self.entered.append(torch.cuda.stream(self.stream))
-        for c in self.entered:
-            c.__enter__()
-        return int(torch.cuda.current_stream().cuda_stream)
+        device, stream = self.device, self.stream
+        if stream is None and device.index == _current_device():
+            return _current_stream(device.index)
+        if stream is not None and stream.device != device:
+            raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+        self.entered = contextlib.ExitStack()
+        self.entered.enter_context(torch.cuda.device(device))
+        if stream is not None:
+            self.entered.enter_context(torch.cuda.stream(stream))
+        return _current_stream(device.index)
 
     def __exit__(self, *exc):
-        while self.entered:
-            self.entered.pop().__exit__(*exc)
+        if self.entered is not None:
+            self.entered.close()
         return False
 
 
@@ -60,6 +66,8 @@ def _same_device(device, **tensors):
 def _matrix(t: torch.Tensor, cols: int) -> torch.Tensor:
     """[..., cols] as [rows, cols] with each row's elements adjacent and rows
     not overlapping (copied where they are not)."""
+    if t.dim() == 2 and t.is_contiguous():
+        return t
     t2 = t if t.dim() == 2 else t.reshape(-1, cols)
     if t2.numel() and (t2.stride(1) != 1 or (t2.shape[0] > 1 and t2.stride(0) < cols)):
         t2 = t2.contiguous()
@@ -102,8 +110,8 @@ def _norm_args(x, weight, eps, residual):
 def _like(out, x, what):
     """An output of x's shape and dtype, allocated when not given; (tensor, 2-D view)."""
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        return out, out.view(-1, x.shape[-1]) if x.dim() != 2 else out
+        out = torch.empty_like(x, memory_format=torch.contiguous_format)
+        return out, out if x.dim() == 2 else out.view(-1, x.shape[-1])
     return out, _given(out, tuple(x.shape), x.device, what, x.dtype)
 
 

@@ -2650,14 +2650,13 @@ int situ_glu_set_load_path(int path) {
 
 int situ_glu_device_status(int clear) {
   if (cudaDeviceSynchronize() != cudaSuccess) return -1;
-  int v = 0;
-  if (cudaMemcpyFromSymbol(&v, g_device_status, sizeof v) != cudaSuccess) return -1;
-  if (clear && v != 0) {
-    const int zero = 0;
-    if (cudaMemcpyToSymbol(g_device_status, &zero, sizeof zero) != cudaSuccess) return -1;
+  int status = 0;
+  for (const int v : {unit_device_status(clear), norm_device_status(clear), moe_device_status(clear),
+                      nvfp4_device_status(clear)}) {
+    if (v < 0) return -1;
+    if (v != 0) status = v;
   }
-  const int nvfp4 = nvfp4_device_status(clear);
-  return nvfp4 != 0 ? nvfp4 : v;
+  return status;
 }
 
 situ_status_t situ_glu_wait_probe(int64_t limit_ns, void* stream) {

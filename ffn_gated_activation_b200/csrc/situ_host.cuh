@@ -94,14 +94,42 @@ inline void fill_coeffs(double beta, int has_lb, double lb, Coeffs* c, int* gate
   *gate_mode = beta == 4.0 ? kGateSquare : beta == 2.0 ? kGateEqual : beta == 1.0 ? kGateRoot : kGateGeneric;
 }
 
+// CTAs of a kernel that one SM holds, asked of the runtime once per (device,
+// kernel, launch shape).
+inline situ_status_t ctas_per_sm(const void* kernel, int threads, int smem, int* per_sm) {
+  struct Entry {
+    int dev;
+    const void* kernel;
+    int threads, smem, per_sm;
+  };
+  static std::mutex mu;
+  static Entry seen[512];
+  static int n_seen = 0;
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return fail(SITU_ERR_CUDA, "cudaGetDevice: %s", cudaGetErrorString(err));
+  std::lock_guard<std::mutex> lock(mu);
+  for (int i = 0; i < n_seen; ++i) {
+    const Entry& e = seen[i];
+    if (e.kernel == kernel && e.threads == threads && e.smem == smem && e.dev == dev) {
+      *per_sm = e.per_sm;
+      return SITU_OK;
+    }
+  }
+  err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(per_sm, kernel, threads, smem);
+  if (err != cudaSuccess || *per_sm <= 0)
+    return fail(SITU_ERR_CUDA, "occupancy query: %s", cudaGetErrorString(err));
+  if (n_seen < 512) seen[n_seen++] = {dev, kernel, threads, smem, *per_sm};
+  return SITU_OK;
+}
+
 inline situ_status_t launch_grid(const void* kernel, int threads, int smem, int64_t tokens, int* grid) {
   int sms = 0;
   situ_status_t st = device_sm_count(&sms);
   if (st != SITU_OK) return st;
   int per_sm = 0;
-  cudaError_t err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, smem);
-  if (err != cudaSuccess || per_sm <= 0)
-    return fail(SITU_ERR_CUDA, "occupancy query: %s", cudaGetErrorString(err));
+  st = ctas_per_sm(kernel, threads, smem, &per_sm);
+  if (st != SITU_OK) return st;
   int64_t g = static_cast<int64_t>(sms) * per_sm;
   const int cap = g_max_ctas.load(std::memory_order_relaxed);
   if (cap > 0 && g > cap) g = cap;
@@ -155,8 +183,24 @@ inline EncodeTiledFn encode_tiled() {
   return fn;
 }
 
-// The status word of the kernels of situ_nvfp4.cu on the current device, read
-// (and, with `clear`, reset) after a synchronisation; -1 on a CUDA error.
+// The status words of the other translation units' kernels on the current
+// device, read (and, with `clear`, reset) after a synchronisation; -1 on a CUDA
+// error.
+int norm_device_status(int clear);
+int moe_device_status(int clear);
 int nvfp4_device_status(int clear);
 
 #pragma GCC visibility pop
+
+// This translation unit's status word, as above.
+namespace {
+[[maybe_unused]] int unit_device_status(int clear) {
+  int v = 0;
+  if (cudaMemcpyFromSymbol(&v, g_device_status, sizeof v) != cudaSuccess) return -1;
+  if (clear && v != 0) {
+    const int zero = 0;
+    if (cudaMemcpyToSymbol(g_device_status, &zero, sizeof zero) != cudaSuccess) return -1;
+  }
+  return v;
+}
+}  // namespace

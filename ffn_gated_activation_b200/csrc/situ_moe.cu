@@ -372,6 +372,8 @@ MoeKernel pick_moe_fc1(int gate) {
 
 }  // namespace
 
+int moe_device_status(int clear) { return unit_device_status(clear); }
+
 extern "C" {
 
 size_t situ_glu_moe_workspace_bytes(int64_t tokens, int64_t topk, int64_t hidden, int64_t inter) {

@@ -82,12 +82,14 @@ __device__ __forceinline__ float row_sum(float v, float* slot, int warps) {
   const int lane = threadIdx.x & 31;
   return warp_sum(lane < warps ? slot[lane] : 0.0f);
 }
+// `BARRIER` names the barrier of the row's threads (0: the whole CTA).
+template <int BARRIER = 0>
 __device__ __forceinline__ float2 row_sum2(float2 v, float2* slot, int warps) {
   v.x = warp_sum(v.x);
   v.y = warp_sum(v.y);
   if (warps == 1) return v;
   if ((threadIdx.x & 31) == 0) slot[threadIdx.x >> 5] = v;
-  __syncthreads();
+  asm volatile("bar.sync %0, %1;" ::"n"(BARRIER), "r"(warps * 32) : "memory");
   const int lane = threadIdx.x & 31;
   const float2 p = lane < warps ? slot[lane] : make_float2(0.0f, 0.0f);
   return make_float2(warp_sum(p.x), warp_sum(p.y));
@@ -172,7 +174,14 @@ __global__ void __launch_bounds__(kNormThreads<V>) situ_rms_norm_fwd_kernel(cons
 // has its own columns) and writes one fp32 row of partial sums; a second kernel
 // adds the chunks in order.  Both orders depend on the shape alone.
 
-constexpr int kNormChunks = 296;  // two per SM of a B200
+// Chunks by the row's width: enough for the CTAs (or, in narrow rows, the warps)
+// that share an SM, few enough that the partial rows stay a few per cent of the
+// traffic.
+constexpr int kNormMaxChunks = 2368;
+int64_t norm_chunks(int64_t tokens, int64_t hidden) {
+  const int64_t most = hidden <= 1024 ? kNormMaxChunks : hidden <= 4096 ? 592 : 296;
+  return tokens < most ? tokens : most;
+}
 
 struct NormBwdArgs {
   const char* gy;
@@ -278,16 +287,179 @@ __global__ void __launch_bounds__(kNormThreads<V>) situ_rms_norm_bwd_kernel(cons
   }
 }
 
-// d_weight[i] = sum of the chunks' partials: 32 columns a CTA, eight groups of
-// chunks side by side, the groups in order at the end.
-constexpr int kNormFinGroups = 8;
+// The same with the rows staged by bulk copies: warp `warps` of the CTA keeps a
+// ring of whole rows (h, grad_y, grad_h) filled, so the next rows' bytes are in
+// flight while this one is summed; without it a CTA's loads wait for its sums
+// (bf16 16384 x 7168: 259 us; staged 146 us, 6.4 TB/s).  V vectors a thread,
+// the thread's weights and its columns' sums in registers.
+struct NormRing {
+  int stages;
+  int stage_bytes;
+};
+
+template <typename S, int V, bool GH>
+__global__ void __launch_bounds__(544) situ_rms_norm_bwd_ring_kernel(const NormBwdArgs a, const NormRing r) {
+  extern __shared__ __align__(128) unsigned char ring[];
+  __shared__ float2 slots[2][32];
+  __shared__ uint64_t full[8], empty[8];
+  const int nt = blockDim.x - 32, warps = nt >> 5;
+  const int row_bytes = a.vpr * kVecBytes;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < r.stages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], warps);
+    }
+    mbar_fence_init();
+  }
+  __syncthreads();
+  int stage = 0;
+  uint32_t phase = 0;
+  if (static_cast<int>(threadIdx.x) >= nt) {
+    // ---- copies: one lane ----
+    if (threadIdx.x == static_cast<unsigned>(nt)) {
+      uint32_t issued = 0;
+      bool ok = true;
+      for (int64_t c = blockIdx.x; ok && c < a.chunks; c += gridDim.x)
+        for (int64_t row = c; row < a.tokens; row += a.chunks) {
+          if (!mbar_wait(&empty[stage], phase ^ 1u)) {
+            atomicExch(&g_device_status, kStatusWaitExpired);
+            ok = false;
+            break;
+          }
+          unsigned char* st = ring + stage * r.stage_bytes;
+          mbar_arrive_expect_tx(&full[stage], (GH ? 3 : 2) * row_bytes);
+          bulk_load(st, a.h + row * a.h_pitch, row_bytes, &full[stage]);
+          bulk_load(st + row_bytes, a.gy + row * a.gy_pitch, row_bytes, &full[stage]);
+          if (GH) bulk_load(st + 2 * row_bytes, a.gh + row * a.gh_pitch, row_bytes, &full[stage]);
+          issued |= 1u << stage;
+          if (++stage == r.stages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      if (!ok)  // let the copies land (bounded) before the CTA exits
+        for (int s = 0; s < r.stages; ++s)
+          if (issued & (1u << s)) mbar_wait(&full[s], s < stage ? phase : phase ^ 1u);
+    }
+    return;
+  }
+  // ---- sums and outputs ----
+  // (four vectors a thread leave no registers for the weights: read from L1 twice a row)
+  constexpr bool kKeep = V < 4;
+  float2 kept[kKeep ? V : 1][S::kPairs], dw[V][S::kPairs];
+  if constexpr (kKeep) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int j = threadIdx.x + i * nt;
+      if (j < a.vpr) norm_weights<S>(a.w, a.w_bf16, j, kept[i]);
+    }
+  }
+  auto weights = [&](int i, float2 (&w)[S::kPairs]) {
+    if constexpr (kKeep) {
+#pragma unroll
+      for (int p = 0; p < S::kPairs; ++p) w[p] = kept[i][p];
+    } else {
+      norm_weights<S>(a.w, a.w_bf16, threadIdx.x + i * nt, w);
+    }
+  };
+  int flip = 0;
+  bool dead = false;  // a wait expired: the control flow goes on, without waits
+  for (int64_t c = blockIdx.x; c < a.chunks; c += gridDim.x) {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+#pragma unroll
+      for (int p = 0; p < S::kPairs; ++p) dw[i][p] = make_float2(0.0f, 0.0f);
+    for (int64_t row = c; row < a.tokens; row += a.chunks) {
+      if (!dead && !mbar_wait(&full[stage], phase)) {
+        atomicExch(&g_device_status, kStatusWaitExpired);
+        dead = true;
+      }
+      const unsigned char* st = ring + stage * r.stage_bytes;
+      uint4 h[V], g[V], gh[V];
+      float2 ss = make_float2(0.0f, 0.0f), gd = ss;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int j = threadIdx.x + i * nt;
+        if (j < a.vpr) {
+          h[i] = lds16(st + j * kVecBytes);
+          g[i] = lds16(st + row_bytes + j * kVecBytes);
+          if (GH) gh[i] = lds16(st + 2 * row_bytes + j * kVecBytes);
+        }
+      }
+      __syncwarp();
+      if ((threadIdx.x & 31) == 0) mbar_arrive(&empty[stage]);  // the warp has its vectors
+      if (++stage == r.stages) {
+        stage = 0;
+        phase ^= 1u;
+      }
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int j = threadIdx.x + i * nt;
+        if (j < a.vpr) {
+          float2 w[S::kPairs];
+          weights(i, w);
+#pragma unroll
+          for (int p = 0; p < S::kPairs; ++p) {
+            const float2 f = as_f2(S::pair(h[i], p));
+            ss = fma2(f, f, ss);
+            gd = fma2(mul2(as_f2(S::pair(g[i], p)), w[p]), f, gd);
+          }
+        }
+      }
+      const float2 sums = row_sum2<1>(make_float2(ss.x + ss.y, gd.x + gd.y), slots[flip], warps);
+      flip ^= 1;
+      const float q = rsqrtf(sums.x * a.inv_hidden + a.eps);
+      const float along = -(q * q * q) * (sums.y * a.inv_hidden);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int j = threadIdx.x + i * nt;
+        if (j < a.vpr) {
+          uint4 o;
+          float2 w[S::kPairs];
+          weights(i, w);
+#pragma unroll
+          for (int p = 0; p < S::kPairs; ++p) {
+            const float2 f = as_f2(S::pair(h[i], p));
+            const float2 gq = mul2(as_f2(S::pair(g[i], p)), splat(q));
+            float2 d = fma2(gq, w[p], mul2(f, splat(along)));
+            if (GH) d = add2(d, as_f2(S::pair(gh[i], p)));
+            S::put(o, p, d);
+            dw[i][p] = fma2(gq, f, dw[i][p]);
+          }
+          st_stream(a.dx + row * a.dx_pitch + static_cast<int64_t>(j) * kVecBytes, o);
+        }
+      }
+    }
+    if (a.partials != nullptr) {
+      float* out = a.partials + c * (static_cast<int64_t>(a.vpr) * 2 * S::kPairs);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int j = threadIdx.x + i * nt;
+        if (j < a.vpr) {
+          float4* p = reinterpret_cast<float4*>(out + static_cast<int64_t>(j) * 2 * S::kPairs);
+#pragma unroll
+          for (int k = 0; k < S::kPairs; k += 2)
+            p[k / 2] = make_float4(dw[i][k].x, dw[i][k].y, dw[i][k + 1].x, dw[i][k + 1].y);
+        }
+      }
+    }
+  }
+}
+
+// d_weight[i] = sum of the chunks' partials: 32 columns a CTA, 32 groups of
+// chunks side by side, the groups in order at the end.  Launched so that it may
+// be resident before the backward ends (its wait below is for the whole grid).
+constexpr int kNormFinGroups = 32;
 __global__ void __launch_bounds__(32 * kNormFinGroups)
     situ_rms_norm_dw_kernel(const float* partials, int64_t chunks, int hidden, void* d_w, int bf16) {
   __shared__ float part[kNormFinGroups][32];
   const int col = blockIdx.x * 32 + threadIdx.x;
   float s = 0.0f;
-  if (col < hidden)
-    for (int64_t c = threadIdx.y; c < chunks; c += kNormFinGroups) s += partials[c * hidden + col];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (col < hidden) {
+#pragma unroll 4
+    for (int64_t c = threadIdx.y; c < chunks; c += kNormFinGroups) s += __ldcg(partials + c * hidden + col);
+  }
   part[threadIdx.y][threadIdx.x] = s;
   __syncthreads();
   if (threadIdx.y == 0 && col < hidden) {
@@ -312,8 +484,6 @@ RowShape row_shape(int vpr) {
   const int v = vpr <= 512 ? 2 : vpr <= 1024 ? 4 : 8;
   return {v, ((vpr + v - 1) / v + 31) / 32 * 32, 1};
 }
-
-int64_t norm_chunks(int64_t tokens) { return tokens < kNormChunks ? tokens : kNormChunks; }
 
 // Checks shared by the three entry points.
 situ_status_t norm_check(situ_dtype_t dtype, int64_t tokens, int64_t hidden, situ_dtype_t weight_dtype, double eps) {
@@ -353,6 +523,37 @@ situ_status_t check_matrices(std::initializer_list<Matrix> ms, int64_t rows) {
   return SITU_OK;
 }
 Span span_of(const Matrix& m, int64_t rows) { return matrix_span(m.p, rows, m.stride, m.width, m.es); }
+
+using NormRingKernel = void (*)(NormBwdArgs, NormRing);
+template <typename S>
+NormRingKernel pick_norm_ring(int v, bool gh) {
+  switch (v) {
+    case 1: return gh ? situ_rms_norm_bwd_ring_kernel<S, 1, true> : situ_rms_norm_bwd_ring_kernel<S, 1, false>;
+    case 2: return gh ? situ_rms_norm_bwd_ring_kernel<S, 2, true> : situ_rms_norm_bwd_ring_kernel<S, 2, false>;
+    default: return gh ? situ_rms_norm_bwd_ring_kernel<S, 4, true> : situ_rms_norm_bwd_ring_kernel<S, 4, false>;
+  }
+}
+
+// Launch of the staged backward: one CTA per SM for rows that need 512 threads,
+// two or more for narrower ones, each with its share of the shared memory.
+situ_status_t launch_norm_ring(const NormBwdArgs& a, bool bf, cudaStream_t s) {
+  const int v = a.vpr <= 256 ? 1 : a.vpr <= 1024 ? 2 : 4;
+  const int nt = ((a.vpr + v - 1) / v + 31) / 32 * 32;
+  const int ctas = nt > 256 ? 1 : nt > 128 ? 2 : 4;
+  NormRing r;
+  r.stage_bytes = (a.gh != nullptr ? 3 : 2) * a.vpr * kVecBytes;
+  r.stages = (208 * 1024 / ctas) / r.stage_bytes;
+  if (r.stages > 8) r.stages = 8;
+  const int smem = r.stages * r.stage_bytes;
+  NormRingKernel k = bf ? pick_norm_ring<Bf16>(v, a.gh != nullptr) : pick_norm_ring<F32>(v, a.gh != nullptr);
+  situ_status_t st = ensure_smem(reinterpret_cast<const void*>(k), smem);
+  if (st != SITU_OK) return st;
+  int grid = 0;
+  st = launch_grid(reinterpret_cast<const void*>(k), nt + 32, smem, a.chunks, &grid);
+  if (st != SITU_OK) return st;
+  k<<<grid, nt + 32, smem, s>>>(a, r);
+  return check_launch("situ_glu_rms_norm_bwd");
+}
 
 using NormFwdKernel = void (*)(NormArgs, MxOut);
 template <typename S, bool MX>
@@ -456,6 +657,8 @@ situ_status_t norm_fwd_entry(const void* x, situ_dtype_t dtype, int64_t tokens, 
 
 }  // namespace
 
+int norm_device_status(int clear) { return unit_device_status(clear); }
+
 extern "C" {
 
 situ_status_t situ_glu_rms_norm_fwd(const void* x, situ_dtype_t dtype, int64_t tokens, int64_t hidden,
@@ -480,7 +683,7 @@ situ_status_t situ_glu_rms_norm_fwd_mxfp8(const void* x, situ_dtype_t dtype, int
 
 size_t situ_glu_rms_norm_bwd_workspace_bytes(int64_t tokens, int64_t hidden, int want_dweight) {
   if (!want_dweight || tokens <= 0 || hidden <= 0 || hidden > kNormMaxRowBytes / 2) return 0;
-  return (static_cast<size_t>(norm_chunks(tokens)) * static_cast<size_t>(hidden) * sizeof(float) + 255) / 256 * 256;
+  return (static_cast<size_t>(norm_chunks(tokens, hidden)) * static_cast<size_t>(hidden) * sizeof(float) + 255) / 256 * 256;
 }
 
 situ_status_t situ_glu_rms_norm_bwd(const void* grad_y, int64_t grad_y_row_stride, const void* grad_h,
@@ -550,26 +753,45 @@ situ_status_t situ_glu_rms_norm_bwd(const void* grad_y, int64_t grad_y_row_strid
   a.dx_pitch = d_x_row_stride * es;
   a.partials = d_weight != nullptr ? static_cast<float*>(workspace) : nullptr;
   a.tokens = tokens;
-  a.chunks = norm_chunks(tokens);
+  a.chunks = norm_chunks(tokens, hidden);
   a.vpr = static_cast<int>(hidden * es / kVecBytes);
   a.eps = static_cast<float>(epsilon);
   a.inv_hidden = static_cast<float>(1.0 / static_cast<double>(hidden));
-  const RowShape rs = row_shape(a.vpr);
-  NormBwdKernel k = dtype == SITU_DTYPE_BF16 ? pick_norm_bwd<Bf16>(rs.v) : pick_norm_bwd<F32>(rs.v);
-  const int smem = rs.v == 8 ? rs.v * rs.threads * (kVecBytes / es) * 4 : 0;
-  if (smem > 48 * 1024) {
-    st = ensure_smem(reinterpret_cast<const void*>(k), smem);
+  const bool bf = dtype == SITU_DTYPE_BF16;
+  // Staged rows from 129 vectors (narrower rows have a warp each and enough of
+  // them in flight) up to 2048, of which two or more fit in shared memory.
+  if (a.vpr > 128 && a.vpr <= 2048) {
+    st = launch_norm_ring(a, bf, s);
+  } else {
+    const RowShape rs = row_shape(a.vpr);
+    NormBwdKernel k = bf ? pick_norm_bwd<Bf16>(rs.v) : pick_norm_bwd<F32>(rs.v);
+    const int smem = rs.v == 8 ? rs.v * rs.threads * (kVecBytes / es) * 4 : 0;
+    if (smem > 48 * 1024) {
+      st = ensure_smem(reinterpret_cast<const void*>(k), smem);
+      if (st != SITU_OK) return st;
+    }
+    int grid = 0;
+    st = launch_grid(reinterpret_cast<const void*>(k), rs.threads * rs.rows, smem, (a.chunks + rs.rows - 1) / rs.rows,
+                     &grid);
     if (st != SITU_OK) return st;
+    k<<<grid, dim3(rs.threads, rs.rows), smem, s>>>(a);
+    st = check_launch("situ_glu_rms_norm_bwd");
   }
-  int grid = 0;
-  st = launch_grid(reinterpret_cast<const void*>(k), rs.threads * rs.rows, smem, (a.chunks + rs.rows - 1) / rs.rows,
-                   &grid);
-  if (st != SITU_OK) return st;
-  k<<<grid, dim3(rs.threads, rs.rows), smem, s>>>(a);
-  st = check_launch("situ_glu_rms_norm_bwd");
   if (st != SITU_OK || d_weight == nullptr) return st;
-  situ_rms_norm_dw_kernel<<<static_cast<int>((hidden + 31) / 32), dim3(32, kNormFinGroups), 0, s>>>(
-      a.partials, a.chunks, static_cast<int>(hidden), d_weight, weight_dtype == SITU_DTYPE_BF16);
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(static_cast<unsigned>((hidden + 31) / 32));
+  cfg.blockDim = dim3(32, kNormFinGroups);
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t err =
+      cudaLaunchKernelEx(&cfg, situ_rms_norm_dw_kernel, static_cast<const float*>(a.partials), a.chunks,
+                         static_cast<int>(hidden), d_weight, weight_dtype == SITU_DTYPE_BF16 ? 1 : 0);
+  if (err != cudaSuccess)
+    return fail(SITU_ERR_CUDA, "situ_glu_rms_norm_bwd (d_weight) launch: %s", cudaGetErrorString(err));
   return check_launch("situ_glu_rms_norm_bwd (d_weight)");
 }
 

@@ -663,20 +663,12 @@ void fill_store(StoreArgs* a, int64_t rows, int64_t cols) {
   a->blocks = rows * (cols / 16);
 }
 
-// Rows without a gap between them are one long row to the kernels' loops.
+// Whether every vector pair of a matrix is 32-byte aligned.
 int wide_rows(const void* p, int64_t pitch) { return aligned(p, 32) && pitch % 32 == 0; }
 
 }  // namespace
 
-int nvfp4_device_status(int clear) {
-  int v = 0;
-  if (cudaMemcpyFromSymbol(&v, g_device_status, sizeof v) != cudaSuccess) return -1;
-  if (clear && v != 0) {
-    const int zero = 0;
-    if (cudaMemcpyToSymbol(g_device_status, &zero, sizeof zero) != cudaSuccess) return -1;
-  }
-  return v;
-}
+int nvfp4_device_status(int clear) { return unit_device_status(clear); }
 
 extern "C" {
 
