@@ -235,10 +235,7 @@ __global__ void __launch_bounds__(kStoreThreads) situ_nvfp4_dequantize_kernel(co
 //   * warps 6 .. bring the block scales.  The tensor cores read them from TMEM in
 //     32-lane x 4-column atoms (512 bytes for 128 rows and 64 elements of k:
 //     row r's four scales at lane r % 32, column r / 32), while memory has them
-//     row by row, 16 bytes for a stage's 256 elements.  A lane loads rows l,
-//     l + 32, l + 64, l + 96, and the transposed 4 x 4 words are four 16-byte
-//     shared-memory stores, one per atom, free of bank conflicts.  Loads run
-//     kAhead stages in front of the stores;
+//     row by row, 16 bytes for a stage's 256 elements (scale_rows below);
 //   * warp 1 copies each stage's atoms to TMEM (tcgen05.cp, in issue order with
 //     the products that read them) and issues four products (k = 64 each);
 //   * two accumulators let warps 2-5 store one tile while the next one runs.
@@ -263,7 +260,6 @@ constexpr int kStageK = 256;           // elements of k per stage
 constexpr int kStageRow = 128;         // their bytes
 constexpr int kSteps = 4;              // products (k = 64) per stage
 constexpr int kAtom = 512;             // bytes of scales of 128 rows and one step
-constexpr int kAhead = 4;              // stages of scales in registers
 constexpr int kMaxExperts = 1024;
 constexpr int kHeader = 256;
 
@@ -328,7 +324,7 @@ __device__ __forceinline__ void umma_nvfp4(uint32_t d, uint64_t adesc, uint64_t 
 // The 16 scales of one row and stage: `words` groups of four (64 elements of
 // k) exist, the others are zero.
 __device__ __forceinline__ uint4 load_scales(const uint8_t* p, int words, int vec) {
-  if (vec && words == 4) return __ldg(reinterpret_cast<const uint4*>(p));
+  if (vec && words >= 4) return __ldg(reinterpret_cast<const uint4*>(p));
   const uint32_t* q = reinterpret_cast<const uint32_t*>(p);
   uint4 r = make_uint4(0, 0, 0, 0);
   if (words > 0) r.x = __ldg(q);
@@ -336,6 +332,48 @@ __device__ __forceinline__ uint4 load_scales(const uint8_t* p, int words, int ve
   if (words > 2) r.z = __ldg(q + 2);
   if (words > 3) r.w = __ldg(q + 3);
   return r;
+}
+
+// One warp's share of a tile's block scales: 128 rows (the first `left` exist)
+// of every stage.  Four stages come in one go: lane (rr, j) = (lane / 4, lane %
+// 4) loads stage j's 16 scales of rows rr, rr + 8, ..., so that four lanes read
+// 64 bytes of a row (a load that took 16 bytes from each of 32 rows cost as much
+// of the L1 and shared-memory path as the products' operands).  The lane then
+// has rows l, l + 32, l + 64, l + 96 for each of its l = 8 q + rr: the words of a
+// step's atom that belong together, stored as one vector when its stage's turn
+// comes.  take(stage) waits for a free stage and gives the address of its first
+// atom (the next step's is `apart` bytes on) or NULL to stop; put(stage) hands
+// the stage over.
+template <class Take, class Put>
+__device__ __forceinline__ bool scale_rows(const uint8_t* rows, int64_t pitch, int64_t left, int k, int k_blocks, int vec,
+                                           int apart, Take take, Put put) {
+  const int lane = threadIdx.x & 31, rr = lane >> 2, j = lane & 3;
+  const uint8_t* p = rows + rr * pitch + j * 16;
+  for (int kg = 0; kg < k_blocks; kg += 4, p += 64) {
+    const int words = (k - (kg + j) * kStageK) / 64;  // <= 0 past the end
+    uint4 v[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      v[i] = 8 * i + rr < left ? load_scales(p + i * 8 * pitch, words, vec) : make_uint4(0, 0, 0, 0);
+    for (int u = 0; u < 4 && kg + u < k_blocks; ++u) {
+      unsigned char* st = take();
+      if (st == nullptr) return false;
+      if (j == u) {
+        st += rr * 16;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          *reinterpret_cast<uint4*>(st + q * 128) = make_uint4(v[q].x, v[q + 4].x, v[q + 8].x, v[q + 12].x);
+          *reinterpret_cast<uint4*>(st + q * 128 + apart) = make_uint4(v[q].y, v[q + 4].y, v[q + 8].y, v[q + 12].y);
+          *reinterpret_cast<uint4*>(st + q * 128 + 2 * apart) = make_uint4(v[q].z, v[q + 4].z, v[q + 8].z, v[q + 12].z);
+          *reinterpret_cast<uint4*>(st + q * 128 + 3 * apart) = make_uint4(v[q].w, v[q + 4].w, v[q + 8].w, v[q + 12].w);
+        }
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the copies to TMEM read them
+      __syncwarp();
+      put();
+    }
+  }
+  return true;
 }
 
 template <int BN>
@@ -497,13 +535,12 @@ __global__ void __launch_bounds__(Shape<BN>::kThreads, 1)
         uint32_t r[16];
         tmem_ld16(taddr + c, r);
         tmem_ld_wait(r);
-        if (!valid) continue;
         float v[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]) * alpha;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          if (c + 8 * h >= cols) continue;
+          if (!valid || c + 8 * h >= cols) continue;
           const float* w = v + 8 * h;
           if (a.out_bf16) {
             *reinterpret_cast<uint4*>(out + (c + 8 * h) * 2) =
@@ -515,6 +552,7 @@ __global__ void __launch_bounds__(Shape<BN>::kThreads, 1)
             o[1] = make_float4(w[4], w[5], w[6], w[7]);
           }
         }
+        __syncwarp();
       }
       tc_fence_before();
       mbar_arrive(&acc_empty[b]);
@@ -530,50 +568,24 @@ __global__ void __launch_bounds__(Shape<BN>::kThreads, 1)
     int stage = 0;
     uint32_t phase = 0;
     bool ok = true;
+    auto take = [&]() -> unsigned char* {
+      if (!wait_or_abort(&empty[stage], phase ^ 1u, abort_flag)) return nullptr;
+      return ring + stage * P::kStageBytes + P::kABytes + P::kBBytes + (is_a ? 0 : kSteps * kAtom + (part - 1) * kAtom);
+    };
+    auto put = [&]() {
+      if (lane == 0) mbar_arrive(&full[stage]);
+      if (++stage == P::kStages) {
+        stage = 0;
+        phase ^= 1u;
+      }
+    };
     for (int t = blockIdx.x; ok && t < total; t += gridDim.x) {
       const Tile tile = decode_tile<kBM>(t, first_tile, lo, hi, a.experts, n_tiles, BN);
       // first row of this warp's 128 and how many of them exist
       const int64_t row0 = is_a ? tile.m0 : static_cast<int64_t>(tile.expert) * a.n + tile.n0 + (part - 1) * 128;
       const int64_t left = is_a ? tile.m_end - tile.m0 : min(a.n - tile.n0, BN) - (part - 1) * 128;
-      const uint8_t* rows[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) rows[j] = lane + 32 * j < left ? base + (row0 + lane + 32 * j) * pitch : nullptr;
-      uint4 v[kAhead][4];
-      auto fetch = [&](uint4 (&w)[4], int kb) {
-        const int words = min(4, (a.k - kb * kStageK) / 64);  // <= 0 past the end
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          w[j] = rows[j] != nullptr ? load_scales(rows[j] + kb * 16, words, vec) : make_uint4(0, 0, 0, 0);
-      };
-#pragma unroll
-      for (int u = 0; u < kAhead; ++u) fetch(v[u], u);
-      for (int kb0 = 0; ok && kb0 < k_blocks; kb0 += kAhead) {
-#pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
-          if (kb0 + u >= k_blocks) break;
-          if (!wait_or_abort(&empty[stage], phase ^ 1u, abort_flag)) {
-            ok = false;
-            break;
-          }
-          // atom of step s: word s of rows l, l + 32, l + 64, l + 96
-          unsigned char* st = ring + stage * P::kStageBytes + P::kABytes + P::kBBytes + lane * 16 +
-                              (is_a ? 0 : kSteps * kAtom + (part - 1) * kAtom);
-          const int apart = is_a ? kAtom : P::kScaleAtoms * kAtom;
-          const uint4(&w)[4] = v[u];
-          *reinterpret_cast<uint4*>(st) = make_uint4(w[0].x, w[1].x, w[2].x, w[3].x);
-          *reinterpret_cast<uint4*>(st + apart) = make_uint4(w[0].y, w[1].y, w[2].y, w[3].y);
-          *reinterpret_cast<uint4*>(st + 2 * apart) = make_uint4(w[0].z, w[1].z, w[2].z, w[3].z);
-          *reinterpret_cast<uint4*>(st + 3 * apart) = make_uint4(w[0].w, w[1].w, w[2].w, w[3].w);
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the copies to TMEM read them
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&full[stage]);
-          fetch(v[u], kb0 + u + kAhead);
-          if (++stage == P::kStages) {
-            stage = 0;
-            phase ^= 1u;
-          }
-        }
-      }
+      ok = scale_rows(base + row0 * pitch, pitch, left, a.k, k_blocks, vec, (is_a ? 1 : P::kScaleAtoms) * kAtom, take,
+                      put);
     }
   }
 
@@ -584,19 +596,401 @@ __global__ void __launch_bounds__(Shape<BN>::kThreads, 1)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(P::kTmemCols) : "memory");
 }
 
+// ---- Two-SM form (tcgen05 cta_group::2) ---------------------------------------
+// A cluster of two CTAs computes a 256 x 256 tile (one product: M = 256, N =
+// 256, k = 64): CTA r stages rows [128 r, 128 r + 128) of the A tile and of the
+// B tile and holds accumulator rows [128 r, ...) in its TMEM.  Per operation of
+// the tensor cores an SM moves 5 / 8 of the one-SM form's operand bytes, and the
+// one-SM form is bound by just these: at 192 columns a stage's 40 KB are written
+// to and read from shared memory in 640 cycles, the products take 384.
+//
+// Each CTA needs its own rows' scales and every column's.  Four warps write them
+// to TMEM themselves (tcgen05.st, each its 32 lanes): the tensor pipe takes about
+// 55 cycles for each 512-byte tcgen05.cp and runs no product meanwhile, 660
+// cycles a stage next to 512 of products (8192 x 7168 x 4096: 154 us that way).
+// The scales of four stages are one TMA box (64 bytes of each row, 64-byte
+// swizzle), issued in line with the codes: loads by the warps themselves waited
+// behind the ring's copies in the memory queue, longer than a register prefetch
+// of four stages covers (141 us for 104).  Lane l of each warp then takes rows l,
+// l + 32, ... and has in its registers just the TMEM columns of its lane.  TMEM
+// holds one accumulator (256 columns) and every ring stage's scales (4 x 48).
+//
+// The epilogue drains the accumulator to registers before it stores (bf16), so
+// the next tile's products wait for the drain alone, and turns rows into whole
+// 128-byte lines through shared memory (16384 x 1024 x 4096 with a 16-byte piece
+// of 32 rows per store: 33 of 87 us).
+//
+// Waits poll with CTA scope; where the other CTA's work is waited for, one
+// acquire at cluster scope follows.  (Polling with cluster scope empties L1 each
+// time and held up the scales' loads: 8192 x 7168 x 4096 took 253 us.)
+
+constexpr int kBN2 = 256, kBM2 = 256;
+constexpr int kPairEpiWarps = 4;
+constexpr int kPairScaleWarps = 4;  // one per quarter of the TMEM lanes
+constexpr int kPairThreads = 32 * (2 + kPairEpiWarps + kPairScaleWarps);
+constexpr int kPairABytes = 128 * kStageRow, kPairBBytes = 128 * kStageRow;
+constexpr int kPairStageBytes = kPairABytes + kPairBBytes;
+constexpr int kPairStages = 4;
+constexpr int kPairScaleRows = 128 + kBN2;               // scales of a stage: A's rows, then B's
+constexpr int kPairGroupBytes = kPairScaleRows * 64;     // of four stages
+constexpr int kPairScaleCols = kPairScaleRows / 32 * 4;  // TMEM columns of a stage's scales
+constexpr int kPairScaleBase = kBN2;
+constexpr int kPairOutBytes = 32 * 128;                  // a warp's piece of the output
+constexpr int kPairSmem = kPairStages * kPairStageBytes + 2 * kPairGroupBytes + kPairEpiWarps * kPairOutBytes;
+static_assert(kPairScaleBase + kPairStages * kPairScaleCols <= 512, "two-SM TMEM overflows");
+constexpr uint32_t kPairIdesc = (1u << 7) | (1u << 10) | (static_cast<uint32_t>(kBN2 >> 3) << 17) | (2u << 27);
+
+using fc1::tma_load_2d_pair;
+using fc1::umma_commit_pair;
+using fc1::umma_commit_pair_local;
+
+__device__ __forceinline__ bool wait_or_abort_acquire(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  if (!wait_or_abort(bar, parity, abort_flag)) return false;
+  (void)mbar_try_wait_cluster(bar, parity);  // completed already: the acquire alone
+  return true;
+}
+
+__device__ __forceinline__ void umma_nvfp4_pair(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t sfa, uint32_t sfb,
+                                                uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+      "l"(adesc), "l"(bdesc), "r"(kPairIdesc), "r"(sfa), "r"(sfb), "r"(accumulate));
+}
+// Arrive on an mbarrier of either CTA after TMEM writes that are complete
+// or reads that are complete (tcgen05.wait) and fenced: nothing in memory hangs
+// on the arrival, and a release at cluster scope would wait for the warp's loads
+// and stores in flight as well (1000 and more cycles a stage).
+__device__ __forceinline__ void mbar_arrive_remote_relaxed(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+// Stores 128 bytes of each of a warp's 32 output rows, row0 + lane's in q:
+// columns [c, c + 8 per_vec) of the tile, `per_vec` of them in 16 bytes, those
+// below `cols` (a multiple of 8) and rows below the expert's end.  Through the
+// warp's 4 KB of shared memory (16-byte chunks swizzled by the row), so that
+// eight lanes write a row's line.
+__device__ __forceinline__ void put_piece(unsigned char* piece, const Args& a, const Tile& tile, int64_t row0,
+                                          const uint32_t* q, int c, int cols, int per_vec) {
+  const int lane = threadIdx.x & 31;
+  __syncwarp();  // the piece before is read
+#pragma unroll
+  for (int v = 0; v < 8; ++v)
+    *reinterpret_cast<uint4*>(piece + lane * 128 + ((v ^ (lane & 7)) * 16)) =
+        make_uint4(q[4 * v], q[4 * v + 1], q[4 * v + 2], q[4 * v + 3]);
+  __syncwarp();
+  const int v = lane & 7;
+  if (c + v * per_vec < cols) {
+    char* out = a.out + row0 * a.out_pitch + static_cast<int64_t>(tile.n0 + c + v * per_vec) * (16 / per_vec);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int r = 4 * i + (lane >> 3);
+      if (row0 + r < tile.m_end)
+        *reinterpret_cast<uint4*>(out + r * a.out_pitch) = lds16(piece + r * 128 + ((v ^ (r & 7)) * 16));
+    }
+  }
+}
+__device__ __forceinline__ uint32_t word(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
+
+__global__ void __launch_bounds__(kPairThreads, 1)
+    situ_nvfp4_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_w,
+                                const __grid_constant__ CUtensorMap tmap_as, const __grid_constant__ CUtensorMap tmap_ws,
+                                const Args a) {
+  extern __shared__ unsigned char smem_raw[];
+  const uint32_t raw_addr = smem_u32(smem_raw);
+  unsigned char* ring = smem_raw + ((1024u - (raw_addr & 1023u)) & 1023u);
+  unsigned char* scales = ring + kPairStages * kPairStageBytes;
+  unsigned char* pieces = scales + 2 * kPairGroupBytes;
+  unsigned char* header = ring + kPairSmem;
+  uint64_t* full = reinterpret_cast<uint64_t*>(header);
+  uint64_t* empty = full + kPairStages;
+  uint64_t* acc_full = empty + kPairStages;
+  uint64_t* acc_empty = acc_full + 1;
+  uint64_t* sf_full = acc_empty + 1;  // [2]: this CTA's scales of four stages
+  uint64_t* sf_empty = sf_full + 2;
+  uint64_t* drain = sf_empty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int64_t* lo = reinterpret_cast<int64_t*>(header + kHeader);
+  int64_t* hi = lo + a.experts;
+  int* first_tile = reinterpret_cast<int*>(hi + a.experts);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const bool leader = rank == 0;
+  const int cl = static_cast<int>(cluster_index()), ncl = static_cast<int>(cluster_count());
+  const int n_tiles = (a.n + kBN2 - 1) / kBN2;
+  const int k_blocks = (a.k + kStageK - 1) / kStageK;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kPairStages; ++s) {
+      mbar_init(&full[s], 1 + 2 * kPairScaleWarps);  // CTA 0's: its TMA warp, both CTAs' scale warps and bytes
+      mbar_init(&empty[s], 1);                       // CTA 0's commit, to both
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&sf_full[b], 1);
+      mbar_init(&sf_empty[b], kPairScaleWarps);
+    }
+    mbar_init(acc_full, 1);
+    mbar_init(acc_empty, 2 * 32 * kPairEpiWarps);
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    mbar_fence_init();
+  }
+  if (warp == 0) scan_experts<kBM2>(a, n_tiles, lane, lo, hi, first_tile);
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(512)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // both CTAs' barriers are initialised before any remote arrival
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  const int total = first_tile[a.experts];
+
+  if (warp == 0) {
+    // ---- codes and scales (both CTAs) ----
+    int stage = 0, group = 0;
+    uint32_t phase = 0, issued = 0;
+    bool ok = true;
+    for (int t = cl; ok && t < total; t += ncl) {
+      const Tile tile = decode_tile<kBM2>(t, first_tile, lo, hi, a.experts, n_tiles, kBN2);
+      const int32_t arow = static_cast<int32_t>(tile.m0 + 128 * rank);
+      const int32_t wrow = tile.expert * a.n + tile.n0 + static_cast<int32_t>(128 * rank);
+      for (int kb = 0; kb < k_blocks; ++kb) {
+        if ((kb & 3) == 0) {  // the scales of stages kb .. kb + 3
+          const int b = group & 1;
+          if (!wait_or_abort(&sf_empty[b], ((group >> 1) & 1) ^ 1, abort_flag)) {
+            ok = false;
+            break;
+          }
+          if (lane == 0) {
+            unsigned char* sc = scales + b * kPairGroupBytes;
+            mbar_arrive_expect_tx(&sf_full[b], kPairGroupBytes);
+            tma_load_2d(sc, &tmap_as, kb * 16, arow, &sf_full[b]);
+            tma_load_2d(sc + 128 * 64, &tmap_ws, kb * 16, tile.expert * a.n + tile.n0, &sf_full[b]);
+          }
+          __syncwarp();
+          ++group;
+        }
+        if (!wait_or_abort(&empty[stage], phase ^ 1u, abort_flag)) {
+          ok = false;
+          break;
+        }
+        if (lane == 0) {
+          unsigned char* st = ring + stage * kPairStageBytes;
+          const uint32_t bar = peer_addr(&full[stage], 0);
+          if (leader) mbar_arrive_expect_tx(&full[stage], 2 * (kPairABytes + kPairBBytes));
+          tma_load_2d_pair(st, &tmap_a, kb * kStageRow, arow, bar);
+          tma_load_2d_pair(st + kPairABytes, &tmap_w, kb * kStageRow, wrow, bar);
+        }
+        __syncwarp();
+        issued |= 1u << stage;
+        if (++stage == kPairStages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+    if (!ok) {
+      // Aborted: let this CTA's scales land, and CTA 0 wait for both CTAs' codes
+      // (they count on its barriers); bounded.
+      for (int g = group > 2 ? group - 2 : 0; g < group; ++g) {
+        const unsigned long long t0 = global_timer_ns();
+        while (!mbar_try_wait(&sf_full[g & 1], (g >> 1) & 1) && global_timer_ns() - t0 < kWaitLimitNs) {
+        }
+      }
+    }
+    if (!ok && leader) {
+      for (int s = 0; s < kPairStages; ++s) {
+        if (!(issued & (1u << s))) continue;
+        const uint32_t ph = (s < stage) ? phase : (phase ^ 1u);
+        const unsigned long long t0 = global_timer_ns();
+        while (!mbar_try_wait_cluster(&full[s], ph) && global_timer_ns() - t0 < kWaitLimitNs) {
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (leader) {
+      // ---- products (CTA 0) ----
+      int stage = 0;
+      uint32_t phase = 0, acc_phase = 0;
+      bool ok = true;
+      for (int t = cl; ok && t < total; t += ncl) {
+        if (!wait_or_abort_acquire(acc_empty, acc_phase ^ 1u, abort_flag)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        for (int kb = 0; kb < k_blocks; ++kb) {
+          if (!wait_or_abort_acquire(&full[stage], phase, abort_flag)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          if (lane == 0) {
+            const uint32_t a_addr = smem_u32(ring + stage * kPairStageBytes), b_addr = a_addr + kPairABytes;
+            const uint32_t sfa = tmem_base + kPairScaleBase + static_cast<uint32_t>(stage * kPairScaleCols);
+            const uint32_t sfb = sfa + kSteps * 4;
+#pragma unroll
+            for (int s = 0; s < kSteps; ++s)
+              umma_nvfp4_pair(tmem_base, smem_desc_sw128(a_addr + s * 32), smem_desc_sw128(b_addr + s * 32), sfa + 4 * s,
+                              sfb + 8 * s, (kb | s) != 0 ? 1u : 0u);
+            umma_commit_pair(&empty[stage]);
+          }
+          __syncwarp();
+          if (++stage == kPairStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (!ok) break;
+        if (lane == 0) umma_commit_pair(acc_full);
+        __syncwarp();
+        acc_phase ^= 1u;
+      }
+      if (!ok || *abort_flag) {
+        if (lane == 0) umma_commit_pair_local(drain);
+        __syncwarp();
+        const unsigned long long t0 = global_timer_ns();
+        while (!mbar_try_wait_cluster(drain, 0) && global_timer_ns() - t0 < kWaitLimitNs) {
+        }
+      }
+    }
+  } else if (warp < 2 + kPairEpiWarps) {
+    // ---- epilogue: one accumulator row per thread ----
+    const int quarter = warp & 3;
+    const double unit_a = static_cast<double>(*a.a_amax) / 2688.0;
+    const uint32_t empty_addr = peer_addr(acc_empty, 0);
+    const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16);
+    unsigned char* piece = pieces + (warp - 2) * kPairOutBytes;
+    uint32_t acc_phase = 0;
+    for (int t = cl; t < total; t += ncl) {
+      const Tile tile = decode_tile<kBM2>(t, first_tile, lo, hi, a.experts, n_tiles, kBN2);
+      const float alpha =
+          static_cast<float>(unit_a * (static_cast<double>(a.w_amax[tile.expert * a.w_amax_stride]) / 2688.0));
+      const int64_t row0 = tile.m0 + 128 * rank + quarter * 32;
+      const int cols = min(kBN2, a.n - tile.n0);
+      if (!wait_or_abort(acc_full, acc_phase, abort_flag)) break;
+      tc_fence_after();
+      if (a.out_bf16) {
+        uint32_t q[kBN2 / 2];
+#pragma unroll
+        for (int c = 0; c < kBN2; c += 16) {
+          uint32_t r[16];
+          tmem_ld16(taddr + c, r);
+          tmem_ld_wait(r);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            q[c / 2 + i] = Bf16::pack(make_float2(__uint_as_float(r[2 * i]) * alpha, __uint_as_float(r[2 * i + 1]) * alpha));
+        }
+        tc_fence_before();
+        mbar_arrive_remote_relaxed(empty_addr);
+#pragma unroll
+        for (int c = 0; c < kBN2; c += 64) put_piece(piece, a, tile, row0, &q[c / 2], c, cols, 8);
+      } else {
+#pragma unroll 1
+        for (int c = 0; c < cols; c += 32) {  // uniform over the warp
+          uint32_t r0[16], r1[16], q[32];
+          tmem_ld16(taddr + c, r0);
+          tmem_ld16(taddr + c + 16, r1);
+          tmem_ld_wait(r0, r1);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            q[i] = __float_as_uint(__uint_as_float(r0[i]) * alpha);
+            q[16 + i] = __float_as_uint(__uint_as_float(r1[i]) * alpha);
+          }
+          put_piece(piece, a, tile, row0, q, c, cols, 4);
+        }
+        tc_fence_before();
+        mbar_arrive_remote_relaxed(empty_addr);
+      }
+      acc_phase ^= 1u;
+    }
+  } else {
+    // ---- block scales (both CTAs): this CTA's rows of A, every column's of B ----
+    const int quarter = warp & 3;
+    const uint32_t lanes = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + kPairScaleBase;
+    int stage = 0, group = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int t = cl; ok && t < total; t += ncl) {
+      for (int kg = 0; ok && kg < k_blocks; kg += 4, ++group) {
+        const int b = group & 1;
+        if (!wait_or_abort(&sf_full[b], (group >> 1) & 1, abort_flag)) {
+          ok = false;
+          break;
+        }
+        for (int u = 0; u < 4 && kg + u < k_blocks; ++u) {
+          if (!wait_or_abort(&empty[stage], phase ^ 1u, abort_flag)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          // stage u's 16 bytes of row l: chunk u of the row's 64, swizzled by (row / 2) % 4
+          const unsigned char* st = scales + b * kPairGroupBytes + lane * 64 + ((u ^ ((lane >> 1) & 3)) * 16);
+          const uint32_t col = lanes + static_cast<uint32_t>(stage * kPairScaleCols);
+          uint4 q[12];
+#pragma unroll
+          for (int c = 0; c < 12; ++c) q[c] = lds16(st + c * 2048);
+          uint32_t r[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) r[i] = word(q[i & 3], i >> 2);  // A: step i / 4, row group i % 4
+          tmem_st16(col, r);
+#pragma unroll
+          for (int h2 = 0; h2 < 2; ++h2) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) r[i] = word(q[4 + (i & 7)], 2 * h2 + (i >> 3));  // B: step 2 h2 + i / 8, group i % 8
+            tmem_st16(col + 16 + 16 * h2, r);
+          }
+          asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_remote_relaxed(peer_addr(&full[stage], 0));
+          if (++stage == kPairStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        __syncwarp();
+        if (ok && lane == 0) mbar_arrive(&sf_empty[b]);  // the warp has read the group
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // neither CTA leaves while the pair's products or copies may touch its memory
+  tc_fence_after();
+  if (warp == 1)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(512) : "memory");
+}
+
 // ---- host ---------------------------------------------------------------------
 
-// 2-D byte tensor map of packed codes [rows, >= inner bytes], boxes of 128
-// bytes x `box_rows` with the 128-byte swizzle.
-situ_status_t code_map(CUtensorMap* m, const void* base, int64_t inner, int64_t rows, int64_t pitch, int box_rows) {
+// 2-D byte tensor map of a matrix [rows, >= inner bytes] in boxes of `box_bytes`
+// x `box_rows`, swizzled over the box's width (128: codes, 64: block scales).
+situ_status_t byte_map(CUtensorMap* m, const void* base, int64_t inner, int64_t rows, int64_t pitch, int box_bytes,
+                       int box_rows) {
   EncodeTiledFn fn = encode_tiled();
   if (fn == nullptr) return fail(SITU_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
   const cuuint64_t dims[2] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(rows)};
   const cuuint64_t strides[1] = {static_cast<cuuint64_t>(pitch)};
-  const cuuint32_t box[2] = {static_cast<cuuint32_t>(kStageRow), static_cast<cuuint32_t>(box_rows)};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(box_bytes), static_cast<cuuint32_t>(box_rows)};
   const cuuint32_t estr[2] = {1, 1};
   const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
-                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        box_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(SITU_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", static_cast<int>(r));
   return SITU_OK;
@@ -607,9 +1001,9 @@ situ_status_t launch(const void* a_data, int64_t a_pitch, const void* w_data, in
                      cudaStream_t s) {
   using P = Shape<BN>;
   CUtensorMap ma, mw;
-  situ_status_t st = code_map(&ma, a_data, a.k / 2, a.tokens, a_pitch, kBM);
+  situ_status_t st = byte_map(&ma, a_data, a.k / 2, a.tokens, a_pitch, kStageRow, kBM);
   if (st != SITU_OK) return st;
-  st = code_map(&mw, w_data, a.k / 2, static_cast<int64_t>(a.experts) * a.n, w_pitch, BN);
+  st = byte_map(&mw, w_data, a.k / 2, static_cast<int64_t>(a.experts) * a.n, w_pitch, kStageRow, BN);
   if (st != SITU_OK) return st;
   int grid = 0;
   st = device_sm_count(&grid);
@@ -623,6 +1017,80 @@ situ_status_t launch(const void* a_data, int64_t a_pitch, const void* w_data, in
   st = ensure_smem(reinterpret_cast<const void*>(situ_nvfp4_gemm_kernel<BN>), smem);
   if (st != SITU_OK) return st;
   situ_nvfp4_gemm_kernel<BN><<<grid, P::kThreads, smem, s>>>(ma, mw, a);
+  return check_launch("situ_glu_nvfp4_gemm");
+}
+
+// Clusters of the two-SM kernel that the device holds at once (0: none), asked
+// of the runtime once per device and shared-memory size.
+situ_status_t pair_clusters(cudaLaunchConfig_t* cfg, int* clusters) {
+  struct Entry {
+    int dev;
+    size_t smem;
+    int clusters;
+  };
+  static std::mutex mu;
+  static Entry seen[64];
+  static int n_seen = 0;
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return fail(SITU_ERR_CUDA, "cudaGetDevice: %s", cudaGetErrorString(err));
+  std::lock_guard<std::mutex> lock(mu);
+  for (int i = 0; i < n_seen; ++i)
+    if (seen[i].dev == dev && seen[i].smem == cfg->dynamicSmemBytes) {
+      *clusters = seen[i].clusters;
+      return SITU_OK;
+    }
+  err = cudaOccupancyMaxActiveClusters(clusters, reinterpret_cast<const void*>(situ_nvfp4_gemm_pair_kernel), cfg);
+  if (err != cudaSuccess) {
+    (void)cudaGetLastError();  // the query's error is not sticky: the one-SM form runs
+    *clusters = 0;
+  }
+  if (n_seen < 64) seen[n_seen++] = {dev, cfg->dynamicSmemBytes, *clusters};
+  return SITU_OK;
+}
+
+// Launches the two-SM form; *done is false (and nothing is launched) where the
+// device or the launch cap has no room for a cluster.
+situ_status_t launch_pair(const void* a_data, int64_t a_pitch, const void* w_data, int64_t w_pitch, const Args& a,
+                          cudaStream_t s, bool* done) {
+  *done = false;
+  const int smem = 1024 + kPairSmem + kHeader + a.experts * 20 + 8;
+  situ_status_t st = ensure_smem(reinterpret_cast<const void*>(situ_nvfp4_gemm_pair_kernel), smem);
+  if (st != SITU_OK) return st;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.gridDim = dim3(2, 1, 1);
+  cfg.blockDim = dim3(kPairThreads, 1, 1);
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int clusters = 0;
+  st = pair_clusters(&cfg, &clusters);
+  if (st != SITU_OK) return st;
+  const int cap = g_max_ctas.load(std::memory_order_relaxed);
+  if (cap > 0 && 2 * clusters > cap) clusters = cap / 2;
+  if (clusters == 0) return SITU_OK;
+  const int64_t most = ((a.tokens + kBM2 - 1) / kBM2 + a.experts - 1) * ((a.n + kBN2 - 1) / kBN2);
+  if (clusters > most) clusters = static_cast<int>(most);
+  const int64_t w_rows = static_cast<int64_t>(a.experts) * a.n;
+  CUtensorMap ma, mw, mas, mws;
+  st = byte_map(&ma, a_data, a.k / 2, a.tokens, a_pitch, kStageRow, 128);
+  if (st != SITU_OK) return st;
+  st = byte_map(&mw, w_data, a.k / 2, w_rows, w_pitch, kStageRow, 128);
+  if (st != SITU_OK) return st;
+  st = byte_map(&mas, a.a_scale, a.k / 16, a.tokens, a.a_scale_pitch, 64, 128);
+  if (st != SITU_OK) return st;
+  st = byte_map(&mws, a.w_scale, a.k / 16, w_rows, a.w_scale_pitch, 64, kBN2);
+  if (st != SITU_OK) return st;
+  cfg.gridDim = dim3(2 * clusters, 1, 1);
+  const cudaError_t err = cudaLaunchKernelEx(&cfg, situ_nvfp4_gemm_pair_kernel, ma, mw, mas, mws, a);
+  if (err != cudaSuccess) return fail(SITU_ERR_CUDA, "situ_glu_nvfp4_gemm launch: %s", cudaGetErrorString(err));
+  *done = true;
   return check_launch("situ_glu_nvfp4_gemm");
 }
 
@@ -848,6 +1316,15 @@ situ_status_t situ_glu_nvfp4_gemm(const void* a_data, int64_t a_data_row_stride,
   int sms = 0;
   st = device_sm_count(&sms);
   if (st != SITU_OK) return st;
+  // The two-SM form wants full 256-row tiles (an expert's last one is half empty
+  // on average), enough of them for every pair of SMs, and scales that TMA can
+  // read (16-byte aligned rows: k a multiple of 256 where they are contiguous).
+  const int64_t pairs = ((tokens + nvgemm::kBM2 - 1) / nvgemm::kBM2) * ((n + nvgemm::kBN2 - 1) / nvgemm::kBN2);
+  if (2 * pairs >= sms && tokens >= 256 * experts && a.a_vec && a.w_vec) {
+    bool done = false;
+    st = nvgemm::launch_pair(a_data, a_data_row_stride, w_data, w_data_row_stride, a, s, &done);
+    if (st != SITU_OK || done) return st;
+  }
   // Narrow tiles where wide ones would leave SMs idle (few rows: the weights'
   // bandwidth is the bound, and more SMs draw more of it).
   const int64_t wide = ((tokens + nvgemm::kBM - 1) / nvgemm::kBM) * ((n + 191) / 192);

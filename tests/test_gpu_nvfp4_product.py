@@ -173,7 +173,15 @@ def check_product(got, a, w, offsets, dtype):
     assert bool((got[~seen] == 3).all())
 
 
-def product_case(tokens, k, n, offsets, seed, device, per_expert=True):
+def padded(scale):
+    """The scales with their rows 16 bytes apart or a multiple of it (k need not be one of 256)."""
+    pitch = -(-scale.shape[-1] // 16) * 16
+    wide = torch.full(scale.shape[:-1] + (pitch,), 0x7F, dtype=torch.uint8, device=scale.device)  # NaNs in the gaps
+    wide[..., :scale.shape[-1]] = scale.view(torch.uint8)
+    return wide[..., :scale.shape[-1]]
+
+
+def product_case(tokens, k, n, offsets, seed, device):
     experts = len(offsets) - 1
     a = stored(make(torch.bfloat16, tokens, k, seed=seed), device)
     parts = [stored(make(torch.bfloat16, n, k, seed=seed + 1 + e, std=0.5 + e), device) for e in range(experts)]
@@ -183,9 +191,10 @@ def product_case(tokens, k, n, offsets, seed, device, per_expert=True):
 
 
 # one and several stages of k with whole and part last ones, part tiles of rows and columns, one
-# and many tiles a CTA, narrow (few tiles) and wide tiles
+# and many tiles a CTA, narrow (few tiles), wide and two-SM tiles
 @pytest.mark.parametrize("tokens,k,n", [(1, 64, 8), (1, 256, 64), (3, 128, 72), (128, 256, 64), (129, 320, 192),
-                                        (200, 1024, 200), (64, 4160, 136), (1000, 576, 3000), (2500, 512, 1544)])
+                                        (200, 1024, 200), (64, 4160, 136), (1000, 576, 3000), (2500, 512, 1544),
+                                        (2600, 768, 1544), (5000, 2304, 1000)])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 def test_product(tokens, k, n, dtype, cuda_device):
     a, w = product_case(tokens, k, n, [0, tokens], seed=tokens + k, device=cuda_device)
@@ -204,6 +213,25 @@ def test_groups(offsets, cuda_device):
     out = torch.full((300, 264), 3.0, dtype=torch.float32, device=cuda_device)
     got = pkg.situ_glu_nvfp4_gemm(a, w, torch.tensor(offsets, device=cuda_device), out_dtype=torch.float32, out=out)
     check_product(got, a, w, offsets, torch.float32)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("k", [64, 320, 1344])
+def test_groups_of_two_sm_tiles(k, dtype, cuda_device):
+    offsets = [3, 700, 700, 2990]
+    a, w = product_case(3000, k, 1608, offsets, seed=17, device=cuda_device)
+    a, w = (a[0], padded(a[1]), a[2]), (w[0], padded(w[1]), w[2])
+    out = torch.full((3000, 1608), 3.0, dtype=dtype, device=cuda_device)
+    got = pkg.situ_glu_nvfp4_gemm(a, w, torch.tensor(offsets, device=cuda_device), out_dtype=dtype, out=out)
+    check_product(got, a, w, offsets, dtype)
+    prev = abi.situ_glu_set_max_ctas(6)  # three clusters, many tiles each
+    try:
+        again = torch.full((3000, 1608), 3.0, dtype=dtype, device=cuda_device)
+        pkg.situ_glu_nvfp4_gemm(a, w, torch.tensor(offsets, device=cuda_device), out_dtype=dtype, out=again)
+        assert torch.equal(again, got)
+    finally:
+        abi.situ_glu_set_max_ctas(prev)
+    assert abi.situ_glu_device_status(0) == 0
 
 
 def test_offsets_outside_the_rows_are_clamped(cuda_device):
