@@ -5,17 +5,27 @@
 //
 // A decoding step reads 6 hidden inter bytes of weights per active expert and
 // does a few operations with each, so the bound is the HBM bandwidth of the
-// weights: every weight is read once, straight from HBM into the registers
-// that feed the tensor cores.  The weights are the 16-row operand of
-// mma.m16n8k16 (the tokens fill its eight columns), so one instruction serves
-// up to eight tokens of an expert; with these row counts the products are a
-// few per cent of the tensor rate and never the limit.
+// weights: every weight is read once.  The tensor cores take them from shared
+// memory where TMA puts them (tcgen05.mma, the weights as the row operand, the
+// tokens as the few columns), so no thread touches a weight.
 //
-// A unit of work is 16 weight rows of one expert against all of that expert's
-// tokens: kernel 1 takes 8 gate rows with their 8 up rows (one thread then
-// holds G and U of the same column and applies the activation at once), kernel
-// 2 takes 16 rows of W2_e.  The four warps of a CTA split the sum over k in
-// 64-wide chunks and add their parts through shared memory in warp order.
+// A unit of work is 128 weight rows of one expert: in kernel 1 64 gate rows and
+// the 64 up rows of the same columns, in kernel 2 128 rows of W2_e.  Each SM has
+// one CTA with a contiguous run of units, and one warp streams their rows, a 32
+// KB stage at a time, through a ring with the token rows of the same k: kernel 1
+// multiplies every token of the call (those that are not the expert's cost
+// columns that the product has anyway), kernel 2 the expert's entries.  128 rows
+// are the tensor cores' tallest product and need the fewest of them, four for 16
+// KB; units of 32 or 64 rows would share out more evenly, but one warp issues
+// twice and four times the products and falls behind HBM.  The SMs that get a
+// unit less leave their bandwidth to the others.
+//
+// What this design is for (7168 x 2048, top 8, one token / 4096 x 1024, 64 slots,
+// 32 experts): weights loaded straight into the registers of mma.sync drain at
+// every unit's end (153 / 218 us); staged in shared memory and multiplied with
+// mma.sync, the warps' loads of the token rows wait behind the ring's copies, and
+// with those staged too the eight warps take longer over a stage than HBM does
+// (139 / 224 us).  This one takes 131 / 172 us, 5.4 and 4.7 TB/s of weights.
 //
 // Which tokens an expert has is worked out by every CTA from the token's
 // choices: a 64-bit token mask per expert, and a running count over the
@@ -23,39 +33,46 @@
 // numbers the rows of the intermediate buffers.  A choice that names an expert
 // twice is one entry with the sum of the weights: the layer is linear in them.
 //
-// Kernel 2 leaves one fp32 row per entry; the CTA that completes the last
-// expert of a 16-column group (a counter per group) adds each token's rows in
-// the order of its choices.  No sum depends on which CTA ran when.
+// Kernel 1 leaves an entry's activations as two bf16 rows, the rounding and its
+// remainder; they are two columns of kernel 2's product, added in its epilogue.
+// Kernel 2 leaves one fp32 row per entry; the CTA that completes the last expert
+// of a group of 128 columns (a counter per group) adds each token's rows in the
+// order of its choices.  No sum depends on which CTA ran when.  Kernel 2 may
+// start before kernel 1 has ended: its weights do not wait for the activations.
 
 #include "situ_host.cuh"
 
 namespace {
 
-constexpr int kMoeThreads = 128;
-constexpr int kMoeWarps = kMoeThreads / 32;
+#include "situ_fused_gemm.cuh"
+
+constexpr int kMoeThreads = 192;  // copies, products, four warps of epilogue
 constexpr int kMoeMaxTokens = 64;
 constexpr int kMoeMaxTopk = 16;
 constexpr int kMoeMaxExperts = 1024;
+constexpr int kMoeMaxEntries = kMoeMaxTokens * kMoeMaxTopk;
 constexpr int64_t kMoeMaxDim = 32768;
-constexpr int kMoeChunk = 64;  // k elements of one warp step
+constexpr int kMoeChunk = 64;                        // k elements of a 128-byte swizzle row
+constexpr int kMoeRows = 128;                        // weight rows of a unit
+constexpr int kMoeChunks = 2;                        // of a stage
+constexpr int kMoeTileBytes = kMoeRows * kMoeChunk * 2;           // one chunk's weights
+constexpr int kMoeWeightBytes = kMoeChunks * kMoeTileBytes;       // of a stage
+constexpr int kMoeTile = 16;                         // entries of one product of kernel 2 (32 columns)
+constexpr int kMoeMaxStages = 8;
+constexpr int kMoeTmemCols = 256;                    // two accumulators of 128
+constexpr int kMoeSmem = 224 * 1024;
 
 struct MoeArgs {
-  const char* x;
-  int64_t x_pitch;           // bytes
   const int64_t* ids;
   int64_t ids_stride;        // elements
   const void* weights;       // NULL: 1
   int64_t weights_stride;    // elements
   int weights_bf16;
-  const char* w1;
-  int64_t w1_pitch;          // bytes
-  const char* w2;
-  int64_t w2_pitch;          // bytes
   char* y;
   int64_t y_pitch;           // bytes
   __nv_bfloat16* act;        // [entries][2][inter]: the rounded activations, then the remainders
   float* part;               // [entries][hidden]
-  int* done;                 // [hidden / 16] experts completed
+  int* done;                 // [column groups] experts completed
   int tokens, topk, experts, hidden, inter;
   Coeffs c;
 };
@@ -63,13 +80,21 @@ struct MoeArgs {
 // The call's routing, in shared memory.
 struct MoePlan {
   unsigned long long mask[kMoeMaxExperts];  // tokens of each expert
-  uint16_t start[kMoeMaxExperts];           // first entry of each expert
-  uint16_t active[kMoeMaxTokens * kMoeMaxTopk];  // experts that have a token, rising
-  int16_t id[kMoeMaxTokens * kMoeMaxTopk];  // [token][choice], -1: none
-  float w[kMoeMaxTokens * kMoeMaxTopk];
-  int warp_active[kMoeWarps], warp_entries[kMoeWarps];
+  float weight[kMoeMaxEntries];             // of each entry
+  uint16_t start[kMoeMaxExperts + 1];       // first entry of each expert
+  uint16_t active[kMoeMaxEntries];          // experts that have a token, rising
+  int16_t id[kMoeMaxEntries];               // [token][choice], -1: none or named before
+  uint8_t token[kMoeMaxEntries];            // of each entry
+  float up[2][16][64];                      // kernel 1: the up halves of 16 tokens, for the gate halves' warps
+  int complete[128];                        // kernel 2: column groups whose experts are all done
+  int warp_active[kMoeThreads / 32], warp_entries[kMoeThreads / 32];
   int n_active;
 };
+
+__device__ __forceinline__ int64_t moe_id(const MoeArgs& a, int t, int j) {
+  const int64_t id = a.ids[t * a.ids_stride + j];
+  return id >= 0 && id < a.experts ? id : -1;
+}
 
 __device__ __forceinline__ void moe_plan(const MoeArgs& a, MoePlan& p) {
   const int n = a.tokens * a.topk;
@@ -77,17 +102,11 @@ __device__ __forceinline__ void moe_plan(const MoeArgs& a, MoePlan& p) {
   __syncthreads();
   for (int i = threadIdx.x; i < n; i += kMoeThreads) {
     const int t = i / a.topk, j = i - t * a.topk;
-    const int64_t id = a.ids[t * a.ids_stride + j];
-    const bool in = id >= 0 && id < a.experts;
-    p.id[i] = static_cast<int16_t>(in ? id : -1);
-    float w = 1.0f;
-    if (a.weights != nullptr) {
-      const int64_t at = t * a.weights_stride + j;
-      w = a.weights_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(a.weights)[at])
-                         : static_cast<const float*>(a.weights)[at];
-    }
-    p.w[i] = w;
-    if (in) atomicOr(&p.mask[id], 1ull << t);
+    const int64_t id = moe_id(a, t, j);
+    bool first = id >= 0;
+    for (int k = 0; k < j; ++k) first = first && moe_id(a, t, k) != id;
+    p.id[i] = static_cast<int16_t>(first ? id : -1);
+    if (first) atomicOr(&p.mask[id], 1ull << t);
   }
   __syncthreads();
   // running counts over the experts: each thread a run of them, then the warps
@@ -125,108 +144,28 @@ __device__ __forceinline__ void moe_plan(const MoeArgs& a, MoePlan& p) {
     if (c > 0) p.active[run_a++] = static_cast<uint16_t>(e);
     run_e += c;
   }
-  if (threadIdx.x == kMoeThreads - 1) p.n_active = run_a;
+  if (threadIdx.x == kMoeThreads - 1) {
+    p.n_active = run_a;
+    p.start[a.experts] = static_cast<uint16_t>(run_e);
+  }
   __syncthreads();
-}
-
-// The weight of entry (e, t): the sum over the token's choices that name e.
-__device__ __forceinline__ float moe_weight(const MoeArgs& a, const MoePlan& p, int e, int t) {
-  float w = 0.0f;
-  for (int j = 0; j < a.topk; ++j)
-    if (p.id[t * a.topk + j] == e) w += p.w[t * a.topk + j];
-  return w;
-}
-
-// The k-th set bit of a token mask (k < its count).
-__device__ __forceinline__ int mask_token(unsigned long long m, int k) {
-  for (int i = 0; i < k; ++i) m &= m - 1;
-  return __ffsll(static_cast<long long>(m)) - 1;
-}
-
-__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                         uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-// D[16 x 8 NT] += A[16 x k] B[8 NT x k]^T over this warp's chunks.  Thread
-// (g, t) = (lane / 4, lane % 4) loads the 16-byte vectors t of rows g and g + 8
-// of A and row g of each B tile; since the sum may run over k in any order, the
-// four words of a vector serve as the k pairs (2t, 2t + 8) of two instructions,
-// the same for A and B.  U chunks are requested before any is used.  PARTS: B
-// rows come as a value and its remainder, `part` bytes apart.
-template <int NT, int PARTS, int U>
-__device__ __forceinline__ void mma_rows(float (&acc)[NT][4], const char* a_lo, const char* a_hi, const char* const (&b)[NT],
-                                         int64_t part, int chunks, int warp) {
-#pragma unroll 1
-  for (int c0 = warp; c0 < chunks; c0 += kMoeWarps * U) {
-    uint4 lo[U][2], hi[U][2];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int c = c0 + u * kMoeWarps;
-      if (c < chunks) {
-#pragma unroll
-        for (int v = 0; v < 2; ++v) {
-          lo[u][v] = ld_stream(a_lo + c * (kMoeChunk * 2) + v * 64);
-          hi[u][v] = ld_stream(a_hi + c * (kMoeChunk * 2) + v * 64);
-        }
-      } else {
-#pragma unroll
-        for (int v = 0; v < 2; ++v) lo[u][v] = hi[u][v] = make_uint4(0, 0, 0, 0);
-      }
+  for (int i = threadIdx.x; i < n; i += kMoeThreads) {
+    const int id = p.id[i];
+    if (id < 0) continue;
+    const int t = i / a.topk;
+    const int entry = p.start[id] + __popcll(p.mask[id] & ((1ull << t) - 1));
+    p.token[entry] = static_cast<uint8_t>(t);
+    float w = 0.0f;
+    for (int j = 0; j < a.topk; ++j) {
+      if (moe_id(a, t, j) != id) continue;
+      const int64_t at = t * a.weights_stride + j;
+      w += a.weights == nullptr  ? 1.0f
+           : a.weights_bf16 != 0 ? __bfloat162float(static_cast<const __nv_bfloat16*>(a.weights)[at])
+                                 : static_cast<const float*>(a.weights)[at];
     }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int c = c0 + u * kMoeWarps;
-      if (c >= chunks) break;  // the same for the whole warp
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int q = 0; q < PARTS; ++q)
-#pragma unroll
-          for (int v = 0; v < 2; ++v) {
-            uint4 bv = make_uint4(0, 0, 0, 0);
-            if (b[n] != nullptr) bv = *reinterpret_cast<const uint4*>(b[n] + q * part + c * (kMoeChunk * 2) + v * 64);
-            mma_bf16(acc[n], lo[u][v].x, hi[u][v].x, lo[u][v].y, hi[u][v].y, bv.x, bv.y);
-            mma_bf16(acc[n], lo[u][v].z, hi[u][v].z, lo[u][v].w, hi[u][v].w, bv.z, bv.w);
-          }
-    }
+    p.weight[entry] = w;
   }
-}
-
-// The warps' parts of a unit, added in warp order: warp w's sum for tile n of
-// lane l at red[(w * 8 + n) * 32 + l].  Tile n's total goes to warp n % 4.
-template <int NT>
-__device__ __forceinline__ void put_parts(float4* red, const float (&acc)[NT][4], int warp, int lane) {
-#pragma unroll
-  for (int n = 0; n < NT; ++n) red[(warp * 8 + n) * 32 + lane] = make_float4(acc[n][0], acc[n][1], acc[n][2], acc[n][3]);
-}
-__device__ __forceinline__ float4 sum_parts(const float4* red, int n, int lane) {
-  float4 s = red[n * 32 + lane];
-#pragma unroll
-  for (int w = 1; w < kMoeWarps; ++w) {
-    const float4 v = red[(w * 8 + n) * 32 + lane];
-    s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
-  }
-  return s;
-}
-
-template <int NT, int U>
-__device__ __forceinline__ void fc1_unit(const MoeArgs& a, const MoePlan& p, float4* red, int e, int col0) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const unsigned long long mask = p.mask[e];
-  const int count = __popcll(mask);
-  const char* rows[NT];
-#pragma unroll
-  for (int n = 0; n < NT; ++n)
-    rows[n] = n * 8 + g < count ? a.x + mask_token(mask, n * 8 + g) * a.x_pitch + t * 16 : nullptr;
-  const char* gate = a.w1 + (static_cast<int64_t>(e) * 2 * a.inter + col0 + g) * a.w1_pitch + t * 16;
-  float acc[NT][4] = {};
-  mma_rows<NT, 1, U>(acc, gate, gate + static_cast<int64_t>(a.inter) * a.w1_pitch, rows, 0, a.hidden / kMoeChunk, warp);
-  put_parts<NT>(red, acc, warp, lane);
+  __syncthreads();
 }
 
 // v as the sum of two bf16 numbers, `apart` elements from each other: 16 bits of
@@ -238,115 +177,388 @@ __device__ __forceinline__ void put_split(__nv_bfloat16* out, int apart, float v
   out[apart] = __float2bfloat16(isfinite(rest) ? rest : 0.0f);
 }
 
-template <int GATE, bool HAS_LB>
-__global__ void __launch_bounds__(kMoeThreads, 4) situ_moe_fc1_kernel(const MoeArgs a) {
-  __shared__ MoePlan plan;
-  __shared__ float4 red[kMoeWarps * 8 * 32];
-  for (int i = blockIdx.x * kMoeThreads + threadIdx.x; i < a.hidden / 16; i += gridDim.x * kMoeThreads) a.done[i] = 0;
-  moe_plan(a, plan);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int blocks = a.inter / 8, units = plan.n_active * blocks;
-  for (int u = blockIdx.x; u < units; u += gridDim.x) {
-    const int e = plan.active[u / blocks], col0 = (u % blocks) * 8;
-    const unsigned long long mask = plan.mask[e];
-    const int count = __popcll(mask), tiles = (count + 7) / 8;
-    if (tiles == 1) fc1_unit<1, 4>(a, plan, red, e, col0);
-    else if (tiles == 2) fc1_unit<2, 2>(a, plan, red, e, col0);
-    else if (tiles <= 4) fc1_unit<4, 2>(a, plan, red, e, col0);
-    else fc1_unit<8, 1>(a, plan, red, e, col0);
-    __syncthreads();
-    for (int n = warp; n < tiles; n += kMoeWarps) {
-      const float4 s = sum_parts(red, n, lane);  // G of tokens 2t, 2t + 1, then U
-      const int k0 = n * 8 + 2 * t;
-      if (k0 < count) {
-        const bool two = k0 + 1 < count;
-        const float2 w = make_float2(moe_weight(a, plan, e, mask_token(mask, k0)),
-                                     two ? moe_weight(a, plan, e, mask_token(mask, k0 + 1)) : 0.0f);
-        const Bits2 gb = {__float_as_uint(s.x), __float_as_uint(s.y)};
-        const Bits2 ub = {__float_as_uint(s.z), __float_as_uint(s.w)};
-        const float2 v = fwd_pair_abs<GATE, HAS_LB, F32>(gb, ub, mul2(w, splat(a.c.bb)), a.c);
-        __nv_bfloat16* out = a.act + static_cast<int64_t>(plan.start[e] + k0) * 2 * a.inter + col0 + g;
-        put_split(out, a.inter, v.x);
-        if (two) put_split(out + 2 * a.inter, a.inter, v.y);
-      }
-    }
-    __syncthreads();
-  }
+// A box of rows of k elements [k0, ...): [chunk of 64 elements][row][128 bytes],
+// the 16-byte pieces of a row swizzled by the row.
+__device__ __forceinline__ void moe_box(uint32_t dst, const CUtensorMap* map, int32_t row, int32_t chunk, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+          dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(row), "r"(chunk), "r"(smem_u32(bar))
+      : "memory");
 }
 
-template <int NT, int U>
-__device__ __forceinline__ void fc2_unit(const MoeArgs& a, const MoePlan& p, float4* red, int e, int row0) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int count = __popcll(p.mask[e]);
-  const char* rows[NT];
+// D[128 x n] (+)= A[128 x 16] B[n x 16]^T, bf16 in, fp32 out.  Operands by their
+// shared-memory descriptors: one is 16 bytes further on for every 1 added to it.
+// The whole warp comes here, one lane (`lead`) issues: operands that are the same
+// for the warp stay in uniform registers, where the instruction wants them.
+// (Descriptors computed anew for every product: 70 to 270 cycles each, 152 / 187
+// us for the calls above.)
+__device__ __forceinline__ void moe_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate,
+                                        uint32_t lead) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(lead)
+      : "memory");
+}
+__device__ __forceinline__ uint32_t moe_idesc(int n) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n >> 3) << 17) | (8u << 24);
+}
+
+// First unit of CTA i of `grid` when `units` are shared out in runs.
+__device__ __forceinline__ int moe_first(int units, int i, int grid) {
+  return static_cast<int>(static_cast<int64_t>(units) * i / grid);
+}
+
+constexpr int kMoeTail = (256 + sizeof(MoePlan) + 1023) / 1024 * 1024;  // barriers and plan, after the ring
+
+// Columns of kernel 1's product: the call's tokens; of kernel 2's largest: two
+// per entry.
+__host__ __device__ constexpr int moe_columns(int tokens, bool fc2) {
+  return (tokens + kMoeTile - 1) / kMoeTile * kMoeTile * (fc2 ? 2 : 1);
+}
+__host__ __device__ constexpr int moe_stage_bytes(int tokens, bool fc2) {
+  return kMoeWeightBytes + moe_columns(tokens, fc2) * kMoeChunk * 2 * kMoeChunks;
+}
+__host__ __device__ constexpr int moe_stages(int tokens, bool fc2) {
+  const int s = (kMoeSmem - 1024 - kMoeTail) / moe_stage_bytes(tokens, fc2);
+  return s < kMoeMaxStages ? s : kMoeMaxStages;
+}
+static_assert(moe_stages(kMoeMaxTokens, true) >= 3, "the ring is too short");
+
+// Shared memory: the ring (1024-byte aligned), the barriers, the plan.
+struct MoeSmem {
+  uint32_t ring;
+  uint64_t *full, *empty, *acc_full, *acc_empty, *drain;
+  uint32_t* tmem_slot;
+  volatile int* abort_flag;
+  MoePlan* plan;
+};
+__device__ __forceinline__ MoeSmem moe_smem(unsigned char* raw, int ring_bytes) {
+  unsigned char* base = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
+  MoeSmem m;
+  m.ring = smem_u32(base);
+  m.full = reinterpret_cast<uint64_t*>(base + ring_bytes);
+  m.empty = m.full + kMoeMaxStages;
+  m.acc_full = m.empty + kMoeMaxStages;
+  m.acc_empty = m.acc_full + 2;
+  m.drain = m.acc_empty + 2;
+  m.tmem_slot = reinterpret_cast<uint32_t*>(m.drain + 1);
+  m.abort_flag = reinterpret_cast<volatile int*>(m.tmem_slot + 1);
+  m.plan = reinterpret_cast<MoePlan*>(base + ring_bytes + 256);
+  return m;
+}
+
+// Both kernels: FC2 false is W1 with the activation, true W2 with the sums.
+template <bool FC2, int GATE, bool HAS_LB>
+__global__ void __launch_bounds__(kMoeThreads, 1)
+    situ_moe_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ CUtensorMap tmap_b,
+                    const MoeArgs a) {
+  extern __shared__ unsigned char smem_raw[];
+  const int stages = moe_stages(a.tokens, FC2), stage_bytes = moe_stage_bytes(a.tokens, FC2);
+  const MoeSmem m = moe_smem(smem_raw, stages * stage_bytes);
+  const MoePlan& plan = *m.plan;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if constexpr (!FC2) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    for (int i = blockIdx.x * kMoeThreads + threadIdx.x; i * kMoeRows < a.hidden; i += gridDim.x * kMoeThreads) a.done[i] = 0;
+  }
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kMoeMaxStages; ++s) {
+      mbar_init(&m.full[s], 1);
+      mbar_init(&m.empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&m.acc_full[b], 1);
+      mbar_init(&m.acc_empty[b], 128);
+    }
+    mbar_init(m.drain, 1);
+    *m.abort_flag = 0;
+    mbar_fence_init();
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(m.tmem_slot)),
+                 "r"(kMoeTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  fc1::tc_fence_before();
+  moe_plan(a, *m.plan);
+  fc1::tc_fence_after();
+  const uint32_t tmem = *m.tmem_slot;
+
+  // Kernel 1: expert by expert.  Kernel 2: column group by column group, every expert.
+  const int n_active = plan.n_active, k = FC2 ? a.inter : a.hidden;
+  const int blocks = FC2 ? (a.hidden + kMoeRows - 1) / kMoeRows : a.inter / (kMoeRows / 2), units = n_active * blocks;
+  const int u0 = moe_first(units, blockIdx.x, gridDim.x), u1 = moe_first(units, blockIdx.x + 1, gridDim.x);
+  const int steps = (k + kMoeChunks * kMoeChunk - 1) / (kMoeChunks * kMoeChunk);  // stages of a unit
+  struct Unit {
+    int expert, block, row;   // row: the first of its weight rows
+    int start, count, tiles;  // the expert's entries, and the products of kernel 2 they take
+    int b_bytes;              // of a stage's columns
+  };
+  constexpr int tile_bytes = 2 * kMoeTile * kMoeChunk * 2 * kMoeChunks;  // columns of 16 entries
+  auto unit = [&](int u) -> Unit {
+    Unit v;
+    v.block = FC2 ? u / n_active : u % blocks;
+    v.expert = plan.active[FC2 ? u - v.block * n_active : u / blocks];
+    v.row = FC2 ? v.expert * a.hidden + v.block * kMoeRows : v.expert * 2 * a.inter + v.block * (kMoeRows / 2);
+    v.start = plan.start[v.expert];
+    v.count = plan.start[v.expert + 1] - v.start;
+    v.tiles = (v.count + kMoeTile - 1) / kMoeTile;
+    v.b_bytes = FC2 ? v.tiles * tile_bytes : stage_bytes - kMoeWeightBytes;
+    return v;
+  };
+
+  if (warp == 0) {
+    // ---- copies ----
+    int stage = 0;
+    uint32_t phase = 0, issued = 0;
+    // one stage of a unit: its weights (with the announcement of all the bytes), then its columns
+    auto weights = [&](const Unit& v, int step, int st) {
+      const uint32_t at = m.ring + st * stage_bytes;
+      mbar_arrive_expect_tx(&m.full[st], kMoeWeightBytes + v.b_bytes);
+      if constexpr (FC2) {
+        moe_box(at, &tmap_w, v.row, step * kMoeChunks, &m.full[st]);
+      } else {  // a chunk's gate rows, then its up rows
 #pragma unroll
-  for (int n = 0; n < NT; ++n)
-    rows[n] = n * 8 + g < count
-                  ? reinterpret_cast<const char*>(a.act + static_cast<int64_t>(p.start[e] + n * 8 + g) * 2 * a.inter) + t * 16
-                  : nullptr;
-  const char* w = a.w2 + (static_cast<int64_t>(e) * a.hidden + row0 + g) * a.w2_pitch + t * 16;
-  float acc[NT][4] = {};
-  mma_rows<NT, 2, U>(acc, w, w + 8 * a.w2_pitch, rows, static_cast<int64_t>(a.inter) * 2, a.inter / kMoeChunk, warp);
-  put_parts<NT>(red, acc, warp, lane);
-}
-
-__global__ void __launch_bounds__(kMoeThreads, 4) situ_moe_fc2_kernel(const MoeArgs a) {
-  __shared__ MoePlan plan;
-  __shared__ float4 red[kMoeWarps * 8 * 32];
-  __shared__ int last;
-  moe_plan(a, plan);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int blocks = a.hidden / 16, units = plan.n_active * blocks;
-  if (plan.n_active == 0) {  // no token has an expert
-    for (int b = blockIdx.x; b < blocks; b += gridDim.x)
-      for (int i = threadIdx.x; i < a.tokens * 16; i += kMoeThreads)
-        *reinterpret_cast<__nv_bfloat16*>(a.y + (i / 16) * a.y_pitch + (b * 16 + i % 16) * 2) = __float2bfloat16(0.0f);
-    return;
-  }
-  for (int u = blockIdx.x; u < units; u += gridDim.x) {
-    const int e = plan.active[u / blocks], block = u % blocks, row0 = block * 16;
-    const int count = __popcll(plan.mask[e]), tiles = (count + 7) / 8;
-    if (tiles == 1) fc2_unit<1, 4>(a, plan, red, e, row0);
-    else if (tiles == 2) fc2_unit<2, 2>(a, plan, red, e, row0);
-    else if (tiles <= 4) fc2_unit<4, 2>(a, plan, red, e, row0);
-    else fc2_unit<8, 1>(a, plan, red, e, row0);
-    __syncthreads();
-    for (int n = warp; n < tiles; n += kMoeWarps) {
-      const float4 s = sum_parts(red, n, lane);  // row g of tokens 2t, 2t + 1, then row g + 8
-      const int k0 = n * 8 + 2 * t;
-      if (k0 < count) {
-        float* out = a.part + static_cast<int64_t>(plan.start[e] + k0) * a.hidden + row0 + g;
-        out[0] = s.x;
-        out[8] = s.z;
-        if (k0 + 1 < count) {
-          out[a.hidden] = s.y;
-          out[a.hidden + 8] = s.w;
+        for (int c = 0; c < kMoeChunks; ++c) {
+          moe_box(at + c * kMoeTileBytes, &tmap_w, v.row, step * kMoeChunks + c, &m.full[st]);
+          moe_box(at + c * kMoeTileBytes + kMoeTileBytes / 2, &tmap_w, v.row + a.inter, step * kMoeChunks + c, &m.full[st]);
+        }
+      }
+    };
+    auto columns = [&](const Unit& v, int step, int st) {
+      const uint32_t at = m.ring + st * stage_bytes + kMoeWeightBytes;
+      if constexpr (FC2) {
+        for (int i = 0; i < v.tiles; ++i)
+          moe_box(at + i * tile_bytes, &tmap_b, 2 * (v.start + i * kMoeTile), step * kMoeChunks, &m.full[st]);
+      } else {
+        moe_box(at, &tmap_b, 0, step * kMoeChunks, &m.full[st]);
+      }
+    };
+    int u = u0, step = 0;  // the next stage to send
+    if constexpr (FC2) {  // the first stages' weights are sent before kernel 1's end
+      const int early = min(stages, (u1 - u0) * steps);
+      if (lane == 0) {
+        Unit v{};
+        for (int i = 0, x = u0, y = 0; i < early; ++i) {
+          if (y == 0) v = unit(x);
+          weights(v, y, i);
+          if (++y == steps) y = 0, ++x;
+        }
+      }
+      asm volatile("griddepcontrol.wait;" ::: "memory");  // kernel 1's activations
+      asm volatile("fence.proxy.async;" ::: "memory");
+      Unit v{};
+      for (int i = 0; i < early; ++i) {
+        if (step == 0) v = unit(u);
+        if (lane == 0) columns(v, step, i);
+        if (++step == steps) step = 0, ++u;
+      }
+      __syncwarp();
+      issued = (1u << early) - 1;
+      stage = early % stages;
+      phase = early == stages ? 1u : 0u;
+    }
+    bool ok = true;
+    for (; ok && u < u1; ++u, step = 0) {
+      const Unit v = unit(u);
+      for (; step < steps; ++step) {
+        if (!fc1::wait_or_abort(&m.empty[stage], phase ^ 1u, m.abort_flag)) {
+          ok = false;
+          break;
+        }
+        if (lane == 0) {
+          weights(v, step, stage);
+          columns(v, step, stage);
+        }
+        __syncwarp();
+        issued |= 1u << stage;
+        if (++stage == stages) {
+          stage = 0;
+          phase ^= 1u;
         }
       }
     }
-    // the CTA that completes the group's last expert adds the tokens' rows
-    __threadfence();
-    __syncthreads();
-    if (threadIdx.x == 0) last = atomicAdd(&a.done[block], 1) == plan.n_active - 1;
-    __syncthreads();
-    if (last) {
-      __threadfence();
-      for (int i = threadIdx.x; i < a.tokens * 16; i += kMoeThreads) {
-        const int tok = i / 16, col = row0 + i % 16;
-        float s = 0.0f;
-        for (int j = 0; j < a.topk; ++j) {
-          const int id = plan.id[tok * a.topk + j];
-          bool first = id >= 0;
-          for (int k = 0; k < j; ++k) first = first && plan.id[tok * a.topk + k] != id;
-          if (first) {
-            const int entry = plan.start[id] + __popcll(plan.mask[id] & ((1ull << tok) - 1));
-            s += __ldcg(a.part + static_cast<int64_t>(entry) * a.hidden + col);
+    if (!ok)  // aborted: let the copies this warp issued land (bounded) before the CTA exits
+      for (int s = 0; s < stages; ++s)
+        if (issued & (1u << s)) mbar_wait(&m.full[s], s < stage ? phase : phase ^ 1u);
+  } else if (warp == 1) {
+    // ---- products ----
+    const int n_cols = FC2 ? 2 * kMoeTile : moe_columns(a.tokens, false);
+    const uint32_t idesc = moe_idesc(n_cols);
+    int stage = 0, it = 0;
+    uint32_t phase = 0, acc_phase = 0;
+    bool ok = true;
+    for (int u = u0; ok && u < u1; ++u, ++it) {
+      const int b = it & 1;
+      if (!fc1::wait_or_abort(&m.acc_empty[b], ((acc_phase >> b) & 1u) ^ 1u, m.abort_flag)) {
+        ok = false;
+        break;
+      }
+      fc1::tc_fence_after();
+      const uint32_t d = tmem + static_cast<uint32_t>(b * (kMoeTmemCols / 2));
+      const int n_tiles = FC2 ? unit(u).tiles : 1;
+      for (int step = 0; step < steps; ++step) {
+        if (!fc1::wait_or_abort(&m.full[stage], phase, m.abort_flag)) {
+          ok = false;
+          break;
+        }
+        fc1::tc_fence_after();
+        const uint32_t at = m.ring + stage * stage_bytes;
+        const uint64_t w = fc1::smem_desc_sw128(at);
+        uint64_t t = fc1::smem_desc_sw128(at + kMoeWeightBytes);
+        const uint64_t t_chunk = FC2 ? 2 * kMoeTile * kMoeChunk * 2 / 16 : n_cols * (kMoeChunk * 2 / 16);
+        for (int i = 0; i < n_tiles; ++i, t += tile_bytes / 16) {
+          const uint32_t di = d + i * 2 * kMoeTile;
+#pragma unroll
+          for (int c = 0; c < kMoeChunks; ++c)
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+              moe_mma(di, w + (c * kMoeTileBytes + s * 32) / 16, t + c * t_chunk + s * 2, idesc,
+                      (step | c | s) != 0 ? 1u : 0u, lane == 0);
+        }
+        if (lane == 0) fc1::umma_commit(&m.empty[stage]);
+        __syncwarp();
+        if (++stage == stages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+      if (!ok) break;
+      if (lane == 0) fc1::umma_commit(&m.acc_full[b]);
+      __syncwarp();
+      acc_phase ^= 1u << b;
+    }
+    if (!ok || *m.abort_flag) {
+      // Aborted: wait (bounded) for this warp's products before TMEM is freed.
+      if (lane == 0) fc1::umma_commit(m.drain);
+      __syncwarp();
+      mbar_wait(m.drain, 0);
+    }
+  } else {
+    // ---- epilogue: one accumulator row per thread ----
+    const int q = warp & 3, row = q * 32 + lane;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(q * 32) << 16);
+    if constexpr (FC2) asm volatile("griddepcontrol.wait;" ::: "memory");  // kernel 1's counters
+    uint32_t acc_phase = 0;
+    int it = 0, turn = 0;
+    bool ok = true;  // false: a wait gave up; the barriers below are still met
+    for (int u = u0; u < u1; ++u, ++it) {
+      const int b = it & 1;
+      const Unit v = unit(u);
+      if (ok && !fc1::wait_or_abort(&m.acc_full[b], (acc_phase >> b) & 1u, m.abort_flag)) ok = false;
+      __syncwarp();
+      fc1::tc_fence_after();
+      const uint32_t taddr = lanes + static_cast<uint32_t>(b * (kMoeTmemCols / 2));
+      if constexpr (FC2) {
+        float* out = a.part + static_cast<int64_t>(v.start) * a.hidden + v.block * kMoeRows + row;
+        const bool in = v.block * kMoeRows + row < a.hidden;
+#pragma unroll 1
+        for (int i = 0; i < v.count; i += 8) {  // eight entries, the value's and the remainder's columns
+          uint32_t r[16];
+          fc1::tmem_ld16(taddr + 2 * i, r);
+          fc1::tmem_ld_wait(r);
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (in && i + j < v.count)
+              out[static_cast<int64_t>(i + j) * a.hidden] = __uint_as_float(r[2 * j]) + __uint_as_float(r[2 * j + 1]);
+          __syncwarp();
+        }
+      } else {
+        // rows 0 .. 63 are the gate halves, 64 .. 127 the up halves of the same columns
+        const unsigned long long mask = plan.mask[v.expert];
+        __nv_bfloat16* out = a.act + static_cast<int64_t>(v.start) * 2 * a.inter + v.block * (kMoeRows / 2) + (row & 63);
+        int entry = 0;
+#pragma unroll 1
+        for (int t = 0; t < a.tokens; t += 16) {
+          const uint32_t some = static_cast<uint32_t>(mask >> t) & 0xffffu;
+          if (some == 0) continue;
+          uint32_t r[16];
+          fc1::tmem_ld16(taddr + t, r);
+          fc1::tmem_ld_wait(r);
+          float(&up)[16][64] = m.plan->up[turn & 1];
+          ++turn;
+          if (q >= 2) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) up[j][row & 63] = __uint_as_float(r[j]);
           }
+          asm volatile("bar.sync 1, 128;" ::: "memory");
+          if (q < 2) {
+#pragma unroll
+            for (int j = 0; j < 16; j += 2) {  // two tokens at a time, the expert's among them stored
+              const uint32_t two = (some >> j) & 3u;
+              if (two == 0) continue;
+              const float2 w = make_float2(two & 1u ? plan.weight[v.start + entry] : 0.0f,
+                                           two & 2u ? plan.weight[v.start + entry + (two & 1u)] : 0.0f);
+              const float2 y =
+                  fwd_pair_abs<GATE, HAS_LB, F32>({r[j], r[j + 1]}, {__float_as_uint(up[j][row]), __float_as_uint(up[j + 1][row])},
+                                                  mul2(w, splat(a.c.bb)), a.c);
+              __nv_bfloat16* o = out + static_cast<int64_t>(entry) * 2 * a.inter;
+              if (two & 1u) put_split(o, a.inter, y.x);
+              if (two & 2u) put_split(o + (two & 1u) * 2 * a.inter, a.inter, y.y);
+              entry += __popc(two);
+            }
+          }
+          __syncwarp();
         }
-        *reinterpret_cast<__nv_bfloat16*>(a.y + tok * a.y_pitch + col * 2) = __float2bfloat16(s);
+      }
+      fc1::tc_fence_before();
+      mbar_arrive(&m.acc_empty[b]);
+      acc_phase ^= 1u << b;
+    }
+    if constexpr (FC2) {
+      const int thread = threadIdx.x - 64;
+      if (n_active == 0) {  // no token has an expert
+        for (int64_t i = blockIdx.x * 128 + thread; i < static_cast<int64_t>(a.tokens) * a.hidden; i += gridDim.x * 128)
+          *reinterpret_cast<__nv_bfloat16*>(a.y + i / a.hidden * a.y_pitch + i % a.hidden * 2) = __float2bfloat16(0.0f);
+      } else if (u0 < u1) {
+        // Count this CTA's experts of each of its column groups; where they were the
+        // last, the group's rows are complete and each token's are added here.
+        __threadfence();
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+        const int b0 = u0 / n_active, groups = (u1 - 1) / n_active - b0 + 1;
+        for (int base = 0; base < groups; base += 128) {
+          const int some = min(128, groups - base);
+          if (thread < some) {
+            const int b = b0 + base + thread;
+            const int mine = min(u1, (b + 1) * n_active) - max(u0, b * n_active);
+            m.plan->complete[thread] = mine == n_active || atomicAdd(&a.done[b], mine) + mine == n_active;
+          }
+          asm volatile("bar.sync 1, 128;" ::: "memory");
+          __threadfence();
+          // thread: four columns of every fourth token
+          const int col4 = (thread & 31) * 4;
+          for (int gi = 0; gi < some; ++gi) {
+            const int col = (b0 + base + gi) * kMoeRows + col4;
+            if (!plan.complete[gi] || col >= a.hidden) continue;
+            for (int tok = thread >> 5; tok < a.tokens; tok += 4) {
+              float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+              for (int j = 0; j < a.topk; ++j) {
+                const int id = plan.id[tok * a.topk + j], e = id >= 0 ? id : 0;
+                const int entry = id >= 0 ? plan.start[e] + __popcll(plan.mask[e] & ((1ull << tok) - 1)) : 0;
+                const float4 p = __ldcg(reinterpret_cast<const float4*>(a.part + static_cast<int64_t>(entry) * a.hidden + col));
+                if (id >= 0) s.x += p.x, s.y += p.y, s.z += p.z, s.w += p.w;
+              }
+              *reinterpret_cast<uint2*>(a.y + tok * a.y_pitch + col * 2) =
+                  make_uint2(Bf16::pack(make_float2(s.x, s.y)), Bf16::pack(make_float2(s.z, s.w)));
+            }
+          }
+          asm volatile("bar.sync 1, 128;" ::: "memory");
+        }
       }
     }
   }
+
+  fc1::tc_fence_before();
+  __syncthreads();
+  fc1::tc_fence_after();
+  if (warp == 1)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kMoeTmemCols) : "memory");
 }
 
 // ---- host ---------------------------------------------------------------------
@@ -356,18 +568,82 @@ struct MoeWorkspace {
 };
 MoeWorkspace moe_workspace(int64_t tokens, int64_t topk, int64_t hidden, int64_t inter) {
   auto up = [](int64_t b) { return static_cast<size_t>((b + 255) / 256 * 256); };
-  return {up(tokens * topk * inter * 4), up(tokens * topk * hidden * 4), up(hidden / 16 * 4)};
+  return {up(tokens * topk * inter * 4), up(tokens * topk * hidden * 4), up((hidden + kMoeRows - 1) / kMoeRows * 4)};
 }
 
-using MoeKernel = void (*)(MoeArgs);
+// [rows, k] bf16 as [k / 64][rows][64], boxes of `box_chunks` x `box_rows` x 64
+// elements with the 128-byte swizzle.
+situ_status_t moe_map(CUtensorMap* m, const void* base, int64_t rows, int64_t k, int64_t pitch_elems, int box_rows,
+                      int box_chunks) {
+  EncodeTiledFn fn = encode_tiled();
+  if (fn == nullptr) return fail(SITU_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+  const cuuint64_t dims[3] = {kMoeChunk, static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(k / kMoeChunk)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(pitch_elems) * 2, kMoeChunk * 2};
+  const cuuint32_t box[3] = {kMoeChunk, static_cast<cuuint32_t>(box_rows), static_cast<cuuint32_t>(box_chunks)};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(SITU_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", static_cast<int>(r));
+  return SITU_OK;
+}
+
+using MoeKernel = void (*)(const CUtensorMap, const CUtensorMap, const MoeArgs);
 template <bool LB>
 MoeKernel pick_moe_fc1(int gate) {
   switch (gate) {
-    case kGateSquare: return situ_moe_fc1_kernel<kGateSquare, LB>;
-    case kGateEqual: return situ_moe_fc1_kernel<kGateEqual, LB>;
-    case kGateRoot: return situ_moe_fc1_kernel<kGateRoot, LB>;
-    default: return situ_moe_fc1_kernel<kGateGeneric, LB>;
+    case kGateSquare: return situ_moe_kernel<false, kGateSquare, LB>;
+    case kGateEqual: return situ_moe_kernel<false, kGateEqual, LB>;
+    case kGateRoot: return situ_moe_kernel<false, kGateRoot, LB>;
+    default: return situ_moe_kernel<false, kGateGeneric, LB>;
   }
+}
+
+struct MoeCall {
+  const void *x, *w1, *w2;
+  int64_t x_stride, w1_stride, w2_stride, experts;
+  bool lb;
+  int gate;
+};
+
+situ_status_t launch_moe(const MoeArgs& a, const MoeCall& c, cudaStream_t s) {
+  CUtensorMap mw1, mx, mw2, ma;
+  situ_status_t st = moe_map(&mw1, c.w1, c.experts * 2 * a.inter, a.hidden, c.w1_stride, kMoeRows / 2, 1);
+  if (st != SITU_OK) return st;
+  st = moe_map(&mx, c.x, a.tokens, a.hidden, c.x_stride, moe_columns(a.tokens, false), kMoeChunks);
+  if (st != SITU_OK) return st;
+  st = moe_map(&mw2, c.w2, c.experts * a.hidden, a.inter, c.w2_stride, kMoeRows, kMoeChunks);
+  if (st != SITU_OK) return st;
+  st = moe_map(&ma, a.act, static_cast<int64_t>(a.tokens) * a.topk * 2, a.inter, a.inter, 2 * kMoeTile, kMoeChunks);
+  if (st != SITU_OK) return st;
+  const MoeKernel k1 = c.lb ? pick_moe_fc1<true>(c.gate) : pick_moe_fc1<false>(c.gate);
+  const MoeKernel k2 = situ_moe_kernel<true, kGateGeneric, false>;
+  const int64_t most = c.experts < static_cast<int64_t>(a.tokens) * a.topk ? c.experts : a.tokens * a.topk;
+  int grid = 0;
+  st = ensure_smem(reinterpret_cast<const void*>(k1), kMoeSmem);
+  if (st != SITU_OK) return st;
+  st = ensure_smem(reinterpret_cast<const void*>(k2), kMoeSmem);
+  if (st != SITU_OK) return st;
+  st = launch_grid(reinterpret_cast<const void*>(k1), kMoeThreads, kMoeSmem, most * (a.inter / (kMoeRows / 2)), &grid);
+  if (st != SITU_OK) return st;
+  k1<<<grid, kMoeThreads, kMoeSmem, s>>>(mw1, mx, a);
+  st = check_launch("situ_glu_moe_fwd (FC1)");
+  if (st != SITU_OK) return st;
+  st = launch_grid(reinterpret_cast<const void*>(k2), kMoeThreads, kMoeSmem, most * ((a.hidden + kMoeRows - 1) / kMoeRows), &grid);
+  if (st != SITU_OK) return st;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(kMoeThreads);
+  cfg.dynamicSmemBytes = kMoeSmem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t err = cudaLaunchKernelEx(&cfg, k2, mw2, ma, a);
+  if (err != cudaSuccess) return fail(SITU_ERR_CUDA, "situ_glu_moe_fwd (FC2) launch: %s", cudaGetErrorString(err));
+  return check_launch("situ_glu_moe_fwd (FC2)");
 }
 
 }  // namespace
@@ -410,6 +686,8 @@ situ_status_t situ_glu_moe_fwd(const void* x, int64_t tokens, int64_t hidden, in
       inter % kMoeChunk != 0 || inter > kMoeMaxDim)
     return fail(SITU_ERR_UNSUPPORTED, "hidden and inter must be positive multiples of %d up to %lld, got %lld and %lld",
                 kMoeChunk, (long long)kMoeMaxDim, (long long)hidden, (long long)inter);
+  if (experts * 2 * inter > INT32_MAX || experts * hidden > INT32_MAX)
+    return fail(SITU_ERR_UNSUPPORTED, "sizes exceed the 32-bit tensor-map coordinates");
   if (x_row_stride < hidden || topk_ids_row_stride < topk ||
       (topk_weights != nullptr && topk_weights_row_stride < topk) || w1_row_stride < hidden ||
       w2_row_stride < inter || y_row_stride < hidden)
@@ -447,17 +725,11 @@ situ_status_t situ_glu_moe_fwd(const void* x, int64_t tokens, int64_t hidden, in
   if (overlap(outs[0], outs[1])) return fail(SITU_ERR_INVALID_ARG, "y overlaps workspace");
 
   MoeArgs a{};
-  a.x = static_cast<const char*>(x);
-  a.x_pitch = x_row_stride * 2;
   a.ids = topk_ids;
   a.ids_stride = topk_ids_row_stride;
   a.weights = topk_weights;
   a.weights_stride = topk_weights_row_stride;
   a.weights_bf16 = topk_weights != nullptr && weights_dtype == SITU_DTYPE_BF16;
-  a.w1 = static_cast<const char*>(w1);
-  a.w1_pitch = w1_row_stride * 2;
-  a.w2 = static_cast<const char*>(w2);
-  a.w2_pitch = w2_row_stride * 2;
   a.y = static_cast<char*>(y);
   a.y_pitch = y_row_stride * 2;
   char* base = static_cast<char*>(workspace);
@@ -471,19 +743,8 @@ situ_status_t situ_glu_moe_fwd(const void* x, int64_t tokens, int64_t hidden, in
   a.inter = static_cast<int>(inter);
   int gate = kGateGeneric;
   fill_coeffs(beta, has_linear_beta, linear_beta, &a.c, &gate);
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const int64_t most = experts < tokens * topk ? experts : tokens * topk;  // experts that can be active
-  MoeKernel k1 = has_linear_beta ? pick_moe_fc1<true>(gate) : pick_moe_fc1<false>(gate);
-  int grid = 0;
-  situ_status_t st = launch_grid(reinterpret_cast<const void*>(k1), kMoeThreads, 0, most * (inter / 8), &grid);
-  if (st != SITU_OK) return st;
-  k1<<<grid, kMoeThreads, 0, s>>>(a);
-  st = check_launch("situ_glu_moe_fwd (FC1)");
-  if (st != SITU_OK) return st;
-  st = launch_grid(reinterpret_cast<const void*>(situ_moe_fc2_kernel), kMoeThreads, 0, most * (hidden / 16), &grid);
-  if (st != SITU_OK) return st;
-  situ_moe_fc2_kernel<<<grid, kMoeThreads, 0, s>>>(a);
-  return check_launch("situ_glu_moe_fwd (FC2)");
+  const MoeCall c = {x, w1, w2, x_row_stride, w1_row_stride, w2_row_stride, experts, has_linear_beta != 0, gate};
+  return launch_moe(a, c, static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

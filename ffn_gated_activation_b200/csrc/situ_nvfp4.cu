@@ -309,16 +309,25 @@ __device__ __forceinline__ uint64_t atom_desc(uint32_t addr) {
   return static_cast<uint64_t>((addr >> 4) & 0x3fffu) | (static_cast<uint64_t>(128 >> 4) << 32) |
          (static_cast<uint64_t>(1) << 46);
 }
-__device__ __forceinline__ void scale_cp(uint32_t tmem, uint64_t desc) {
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
+// The whole warp comes here and one lane (`lead`) issues, so that the operands
+// stay in uniform registers; the same for the product below.
+__device__ __forceinline__ void scale_cp(uint32_t tmem, uint64_t desc, uint32_t lead) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %2, 0;\n\t"
+      "@q tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n\t}" ::"r"(tmem),
+      "l"(desc), "r"(lead)
+      : "memory");
 }
 __device__ __forceinline__ void umma_nvfp4(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t sfa,
-                                           uint32_t sfb, uint32_t accumulate) {
+                                           uint32_t sfb, uint32_t accumulate, uint32_t lead) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.b32 p, %6, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate));
+      "setp.ne.b32 q, %7, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate), "r"(lead)
+      : "memory");
 }
 
 // The 16 scales of one row and stage: `words` groups of four (64 elements of
@@ -480,19 +489,18 @@ __global__ void __launch_bounds__(Shape<BN>::kThreads, 1)
           break;
         }
         tc_fence_after();
-        if (lane == 0) {
-          const uint32_t a_addr = smem_u32(ring + stage * P::kStageBytes), b_addr = a_addr + P::kABytes;
-          const uint32_t sc = b_addr + P::kBBytes;
-          const uint32_t sfa = tmem_base + P::kScaleBase + static_cast<uint32_t>(buf * P::kScaleCols);
-          const uint32_t sfb = sfa + kSteps * 4;
+        const uint32_t a_addr = smem_u32(ring + stage * P::kStageBytes);
+        const uint64_t adesc = smem_desc_sw128(a_addr), bdesc = smem_desc_sw128(a_addr + P::kABytes);
+        const uint64_t sc = atom_desc(a_addr + P::kABytes + P::kBBytes);
+        const uint32_t sfa = tmem_base + P::kScaleBase + static_cast<uint32_t>(buf * P::kScaleCols);
+        const uint32_t sfb = sfa + kSteps * 4;
 #pragma unroll
-          for (int i = 0; i < kSteps * (1 + P::kScaleAtoms); ++i) scale_cp(sfa + 4 * i, atom_desc(sc + i * kAtom));
+        for (int i = 0; i < kSteps * (1 + P::kScaleAtoms); ++i) scale_cp(sfa + 4 * i, sc + i * (kAtom / 16), lane == 0);
 #pragma unroll
-          for (int s = 0; s < kSteps; ++s)
-            umma_nvfp4(d, smem_desc_sw128(a_addr + s * 32), smem_desc_sw128(b_addr + s * 32), P::kIdesc, sfa + 4 * s,
-                       sfb + 4 * P::kScaleAtoms * s, (kb | s) != 0 ? 1u : 0u);
-          umma_commit(&empty[stage]);
-        }
+        for (int s = 0; s < kSteps; ++s)
+          umma_nvfp4(d, adesc + 2 * s, bdesc + 2 * s, P::kIdesc, sfa + 4 * s, sfb + 4 * P::kScaleAtoms * s,
+                     (kb | s) != 0 ? 1u : 0u, lane == 0);
+        if (lane == 0) umma_commit(&empty[stage]);
         __syncwarp();
         buf ^= 1;
         if (++stage == P::kStages) {
@@ -650,13 +658,17 @@ __device__ __forceinline__ bool wait_or_abort_acquire(uint64_t* bar, uint32_t pa
   return true;
 }
 
+// The whole warp comes here and one lane (`lead`) issues, so that the operands
+// stay in uniform registers.
 __device__ __forceinline__ void umma_nvfp4_pair(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t sfa, uint32_t sfb,
-                                                uint32_t accumulate) {
+                                                uint32_t accumulate, uint32_t lead) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.b32 p, %6, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
-      "l"(adesc), "l"(bdesc), "r"(kPairIdesc), "r"(sfa), "r"(sfb), "r"(accumulate));
+      "setp.ne.b32 q, %7, 0;\n\t"
+      "@q tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+      "l"(adesc), "l"(bdesc), "r"(kPairIdesc), "r"(sfa), "r"(sfb), "r"(accumulate), "r"(lead)
+      : "memory");
 }
 // Arrive on an mbarrier of either CTA after TMEM writes that are complete
 // or reads that are complete (tcgen05.wait) and fenced: nothing in memory hangs
@@ -838,16 +850,15 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             break;
           }
           tc_fence_after();
-          if (lane == 0) {
-            const uint32_t a_addr = smem_u32(ring + stage * kPairStageBytes), b_addr = a_addr + kPairABytes;
-            const uint32_t sfa = tmem_base + kPairScaleBase + static_cast<uint32_t>(stage * kPairScaleCols);
-            const uint32_t sfb = sfa + kSteps * 4;
+          const uint32_t a_addr = smem_u32(ring + stage * kPairStageBytes);
+          const uint64_t adesc = smem_desc_sw128(a_addr), bdesc = smem_desc_sw128(a_addr + kPairABytes);
+          const uint32_t sfa = tmem_base + kPairScaleBase + static_cast<uint32_t>(stage * kPairScaleCols);
+          const uint32_t sfb = sfa + kSteps * 4;
 #pragma unroll
-            for (int s = 0; s < kSteps; ++s)
-              umma_nvfp4_pair(tmem_base, smem_desc_sw128(a_addr + s * 32), smem_desc_sw128(b_addr + s * 32), sfa + 4 * s,
-                              sfb + 8 * s, (kb | s) != 0 ? 1u : 0u);
-            umma_commit_pair(&empty[stage]);
-          }
+          for (int s = 0; s < kSteps; ++s)
+            umma_nvfp4_pair(tmem_base, adesc + 2 * s, bdesc + 2 * s, sfa + 4 * s, sfb + 8 * s, (kb | s) != 0 ? 1u : 0u,
+                            lane == 0);
+          if (lane == 0) umma_commit_pair(&empty[stage]);
           __syncwarp();
           if (++stage == kPairStages) {
             stage = 0;

@@ -517,7 +517,7 @@ situ_status_t situ_glu_moe_fwd(const void *x, int64_t tokens, int64_t hidden, in
                                void *workspace, size_t workspace_bytes, void *stream);
 
 /* Bytes of workspace situ_glu_moe_fwd needs: per (token, choice) the activations
- * as two bf16 rows of inter and an fp32 row of hidden, and a counter per 16
+ * as two bf16 rows of inter and an fp32 row of hidden, and a counter per 128
  * columns of y, each rounded up to 256. */
 size_t situ_glu_moe_workspace_bytes(int64_t tokens, int64_t topk, int64_t hidden, int64_t inter);
 

@@ -111,7 +111,7 @@ def test_workspace_queries(native_lib_path):
     assert q(100_000, 7168, 1) == 296 * 7168 * 4  # one row of sums per chunk, at most 296 chunks
     assert q(8, 1 << 20, 1) == 0
     m = abi.situ_glu_moe_workspace_bytes
-    assert m(1, 8, 7168, 2048) == 8 * 2048 * 4 + 8 * 7168 * 4 + 448 * 4
+    assert m(1, 8, 7168, 2048) == 8 * 2048 * 4 + 8 * 7168 * 4 + 256
     assert m(65, 8, 7168, 2048) == 0 and m(0, 8, 64, 64) == 0 and m(1, 17, 64, 64) == 0
 
 
