@@ -6,6 +6,8 @@
 // s_b = E4M3(amax_b 448 / A) and the codes E2M1(x 2688 / (A s_b)); a code q
 // stands for q s_b A / 2688.
 
+#include <type_traits>
+
 #include "situ_host.cuh"
 
 namespace {
@@ -37,17 +39,21 @@ struct StoreArgs {
   int64_t blocks;       // rows * per_row
   uint32_t per_row;     // blocks of 16 elements
   int wide;             // the matrix' vectors are 32-byte aligned
+  int flat;             // no gaps between rows anywhere: one long row
 };
 
 // Row and column block of block i.
-__device__ __forceinline__ void block_at(const StoreArgs& a, int64_t i, int64_t& row, uint32_t& col) {
-  if (a.blocks <= 0xffffffffll) {
+__device__ __forceinline__ void block_at(const StoreArgs& a, int64_t i, int64_t& row, int64_t& col) {
+  if (a.flat) {
+    row = 0;
+    col = i;
+  } else if (a.blocks <= 0xffffffffll) {
     const uint32_t r = static_cast<uint32_t>(i) / a.per_row;
     row = r;
     col = static_cast<uint32_t>(i) - r * a.per_row;
   } else {
     row = i / a.per_row;
-    col = static_cast<uint32_t>(i - row * a.per_row);
+    col = i - row * a.per_row;
   }
 }
 
@@ -71,31 +77,89 @@ __device__ __forceinline__ float2 block_pair(const uint4 (&v)[8 / S::kPairs], in
   return as_f2(S::pair(v[p / S::kPairs], p % S::kPairs));
 }
 
-// The largest finite magnitude: per-thread maxima, one integer atomicMax per
-// warp (non-negative floats order as integers), so the result is order-free.
+// The largest magnitude of a block, NaN if there is one.
+template <typename S>
+__device__ __forceinline__ float block_max(const uint4 (&v)[8 / S::kPairs]) {
+  if constexpr (S::kPairs == 4) {  // two bf16 at a time
+    uint32_t m = 0;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(w[i] & 0x7fff7fffu));
+    }
+    return max_nan(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
+  } else {
+    float m = 0.0f;
+#pragma unroll
+    for (int p = 0; p < 8; ++p) {
+      const float2 f = block_pair<S>(v, p);
+      m = max_nan(m, max_nan(fabsf(f.x), fabsf(f.y)));
+    }
+    return m;
+  }
+}
+
+// The same of its finite elements.
+template <typename S>
+__device__ __forceinline__ float block_finite_max(const uint4 (&v)[8 / S::kPairs]) {
+  float m = block_max<S>(v);
+  if (m <= 3.402823466e38f) return m;
+  m = 0.0f;
+#pragma unroll
+  for (int p = 0; p < 8; ++p) {
+    const float2 f = block_pair<S>(v, p);
+    const float ax = fabsf(f.x), ay = fabsf(f.y);
+    m = ax <= 3.402823466e38f ? fmaxf(m, ax) : m;  // false for NaN and infinity
+    m = ay <= 3.402823466e38f ? fmaxf(m, ay) : m;
+  }
+  return m;
+}
+
+// Where block i of the matrix lies, and its elements.
+template <typename S>
+__device__ __forceinline__ void get_block(const StoreArgs& a, int64_t i, int64_t& row, int64_t& col,
+                                          uint4 (&v)[8 / S::kPairs]) {
+  block_at(a, i, row, col);
+  load_block<S>(a.x + row * a.x_pitch + col * (8 / S::kPairs * kVecBytes), a.wide, v);
+}
+
+// The largest finite magnitude: per-thread maxima, one integer atomicMax per CTA
+// (non-negative floats order as integers), so the result is order-free.
 template <typename S>
 __global__ void __launch_bounds__(kStoreThreads) situ_nvfp4_amax_kernel(const StoreArgs a) {
   float m = 0.0f;
   const int64_t step = static_cast<int64_t>(gridDim.x) * kStoreThreads;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kStoreThreads + threadIdx.x; i < a.blocks; i += step) {
-    int64_t row;
-    uint32_t col;
-    block_at(a, i, row, col);
-    uint4 v[8 / S::kPairs];
-    load_block<S>(a.x + row * a.x_pitch + static_cast<int64_t>(col) * (8 / S::kPairs * kVecBytes), a.wide, v);
-#pragma unroll
-    for (int p = 0; p < 8; ++p) {
-      const float2 f = block_pair<S>(v, p);
-      const float ax = fabsf(f.x), ay = fabsf(f.y);
-      m = ax <= 3.402823466e38f ? fmaxf(m, ax) : m;  // false for NaN and infinity
-      m = ay <= 3.402823466e38f ? fmaxf(m, ay) : m;
-    }
+  int64_t i = static_cast<int64_t>(blockIdx.x) * kStoreThreads + threadIdx.x, row;
+  int64_t col;
+  uint4 u[8 / S::kPairs], v[8 / S::kPairs];
+  for (; i + step < a.blocks; i += 2 * step) {  // two blocks in flight
+    get_block<S>(a, i, row, col, u);
+    get_block<S>(a, i + step, row, col, v);
+    m = fmaxf(m, fmaxf(block_finite_max<S>(u), block_finite_max<S>(v)));
   }
-  const unsigned int bits = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
-  if ((threadIdx.x & 31) == 0 && bits != 0u) atomicMax(a.amax_out, bits);
+  if (i < a.blocks) {
+    get_block<S>(a, i, row, col, u);
+    m = fmaxf(m, block_finite_max<S>(u));
+  }
+  __shared__ unsigned int warp_max[kStoreThreads / 32];
+  unsigned int bits = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
+  if ((threadIdx.x & 31) == 0) warp_max[threadIdx.x >> 5] = bits;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+#pragma unroll
+    for (int w = 1; w < kStoreThreads / 32; ++w) bits = max(bits, warp_max[w]);
+    if (bits != 0u) atomicMax(a.amax_out, bits);
+  }
 }
 
-// Correctly rounded codes.  The fp32 quotients below are within 2^-22 of the
+// Correctly rounded codes.  bf16 elements under an A of at most 12 significant
+// bits (a bf16 tensor's own maximum, say): x 2688 has 13 bits, A s_b 16, and their
+// quotient is either a midpoint of E2M1 or at least 2^-19 away from it.  One
+// correction by the exact residual makes a quotient that fp32 can hold exact (P.
+// Markstein, 1990), so ties come out as ties and nothing else crosses.
+//
+// In general the fp32 quotients below are within 2^-22 of the
 // exact ones, so a code can differ from the exact quotient's only where moving
 // the quotient by 2^-20 either way changes it; there the exact products on
 // both sides of the midpoint are compared in double (all of them have at most
@@ -119,71 +183,163 @@ __device__ __forceinline__ uint32_t exact_scale(float m, float big, float r) {
 }
 // The magnitude code of E2M1(m 2688 / (big s)) where lo and hi are the codes of
 // the quotient moved down and up.
-__device__ __noinline__ uint32_t exact_code(float m, double big_s, uint32_t lo, uint32_t hi) {
+__device__ __forceinline__ uint32_t exact_code(float m, double big_s, uint32_t lo, uint32_t hi) {
   const uint32_t twice = 0xC8643210u;  // 2 x the magnitudes 0, .5, 1, 1.5, 2, 3, 4 of the codes 0 .. 6 (6 is 12: C)
   const double mid = 0.25 * (static_cast<double>((twice >> (4 * lo)) & 15u) + static_cast<double>((twice >> (4 * hi)) & 15u));
   const double left = static_cast<double>(m) * 2688.0, right = mid * big_s;
   return left > right || (left == right && (hi & 1) == 0) ? hi : lo;
 }
+// The codes of eight elements where `down` and `up` differ: a tie, as a rule (one
+// element in a thousand of bf16 data), one element at a time.
+__device__ __noinline__ uint32_t exact_codes(float2 f0, float2 f1, float2 f2, float2 f3, float big, float s, uint32_t down,
+                                             uint32_t up) {
+  const double big_s = static_cast<double>(big) * static_cast<double>(s);
+  const float f[8] = {f0.x, f0.y, f1.x, f1.y, f2.x, f2.y, f3.x, f3.y};
+  uint32_t diff = down ^ up;
+  while (diff != 0) {
+    const int at = (__ffs(static_cast<int>(diff)) - 1) & ~3;
+    float m = 0.0f;
+#pragma unroll
+    for (int p = 0; p < 8; ++p) m = at == 4 * p ? fabsf(f[p]) : m;
+    const uint32_t code = exact_code(m, big_s, (down >> at) & 7u, (up >> at) & 7u);
+    down = (down & ~(7u << at)) | (code << at);
+    diff &= ~(15u << at);
+  }
+  return down;
+}
+
+// The tensor scale of a quantisation: A (2688 where it is 0 or not finite, S_enc
+// = 1), and for a tiny A both sides times 2^80, exactly, so that 448 / A stays
+// finite.
+struct TensorScale {
+  float lift, big, r448, s_enc;
+  bool short_big;  // at most 12 significant bits
+  __device__ __forceinline__ explicit TensorScale(float amax) {
+    big = amax > 0.0f && amax <= 3.402823466e38f ? amax : 2688.0f;
+    lift = big < 0x1p-60f ? 0x1p80f : 1.0f;
+    big *= lift;
+    r448 = 448.0f / big;
+    s_enc = 2688.0f / big;
+    short_big = (__float_as_uint(big) & 0xfffu) == 0 && big >= 0x1p-60f && big <= 0x1p60f && lift == 1.0f;
+  }
+};
+
+template <typename S, bool EXACT>
+__device__ __forceinline__ void quantize_block(const StoreArgs& a, const TensorScale& t, int64_t row, int64_t col,
+                                               uint4 (&v)[8 / S::kPairs]) {
+  const float m = block_max<S>(v);
+  const bool special = !(m <= 3.402823466e38f);
+  const uint32_t sc = special ? 0x7fu : exact_scale(m * t.lift, t.big, t.r448);
+  if (!EXACT && t.lift != 1.0f) {  // a power of two: exact in either type (too large is infinite, and saturates)
+#pragma unroll
+    for (int p = 0; p < 8; ++p)
+      S::put(v[p / S::kPairs], p % S::kPairs, mul2(block_pair<S>(v, p), splat(t.lift)));
+  }
+  uint32_t q[2] = {0u, 0u};
+  if (!special) {
+    const float s = e4m3_value(sc);
+    const float inv = s > 0.0f ? __fdividef(t.s_enc, s) : 0.0f;  // 2 ulp
+    if constexpr (EXACT) {
+      const float2 d = splat(-(t.big * s)), r = splat(inv), r1 = splat(inv * (1.0f / 2688.0f));
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float2 w[4];
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+          const float2 f = block_pair<S>(v, 4 * h + p);
+          const float2 w0 = mul2(f, r);
+          w[p] = fma2(fma2(w0, d, mul2(f, splat(2688.0f))), r1, w0);
+        }
+        q[h] = e2m1x8(w);
+      }
+    } else {
+      const float2 up = splat(inv * kUp), down = splat(inv * kDown);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float2 u[4], d[4];
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+          const float2 f = block_pair<S>(v, 4 * h + p);
+          u[p] = mul2(f, up);
+          d[p] = mul2(f, down);
+        }
+        const uint32_t hi = e2m1x8(u), lo = e2m1x8(d);
+        q[h] = lo;
+        if (lo != hi)
+          q[h] = exact_codes(block_pair<S>(v, 4 * h), block_pair<S>(v, 4 * h + 1), block_pair<S>(v, 4 * h + 2),
+                             block_pair<S>(v, 4 * h + 3), t.big, s, lo, hi);
+      }
+    }
+  }
+  st_stream8(a.data + row * a.data_pitch + col * 8, make_uint2(q[0], q[1]));
+  a.scale[row * a.scale_pitch + col] = static_cast<uint8_t>(sc);
+}
+
+// Blocks [0, blocks) from the end: what the pass before read last may still be in
+// L2; a thread's next block is on its way while this one is coded.
+template <typename S, bool EXACT>
+__device__ __forceinline__ void quantize_blocks(const StoreArgs& a, const TensorScale& t, int64_t k, int64_t step) {
+  int64_t row, next_row, col, next_col;
+  if (k >= a.blocks) return;
+  uint4 v[8 / S::kPairs], next[8 / S::kPairs];
+  get_block<S>(a, a.blocks - 1 - k, row, col, v);
+  for (;;) {
+    k += step;
+    const bool more = k < a.blocks;
+    if (more) get_block<S>(a, a.blocks - 1 - k, next_row, next_col, next);
+    quantize_block<S, EXACT>(a, t, row, col, v);
+    if (!more) break;
+#pragma unroll
+    for (int i = 0; i < 8 / S::kPairs; ++i) v[i] = next[i];
+    row = next_row;
+    col = next_col;
+  }
+}
 
 template <typename S>
 __global__ void __launch_bounds__(kStoreThreads) situ_nvfp4_quantize_kernel(const StoreArgs a) {
-  float big = *a.amax;
-  if (!(big > 0.0f && big <= 3.402823466e38f)) big = 2688.0f;  // S_enc = 1
-  // a tiny A: both sides times 2^80, exactly, so that 448 / A stays finite
-  const float lift = big < 0x1p-60f ? 0x1p80f : 1.0f;
-  big *= lift;
-  const float r448 = 448.0f / big, s_enc = 2688.0f / big;
+  const TensorScale t(*a.amax);
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * kStoreThreads + threadIdx.x;
   const int64_t step = static_cast<int64_t>(gridDim.x) * kStoreThreads;
-  // from the end: what the pass before read last may still be in L2
-  for (int64_t k = static_cast<int64_t>(blockIdx.x) * kStoreThreads + threadIdx.x; k < a.blocks; k += step) {
-    int64_t row;
-    uint32_t col;
-    block_at(a, a.blocks - 1 - k, row, col);
-    uint4 v[8 / S::kPairs];
-    load_block<S>(a.x + row * a.x_pitch + static_cast<int64_t>(col) * (8 / S::kPairs * kVecBytes), a.wide, v);
-    float2 f[8];
-    float m = 0.0f;
-#pragma unroll
-    for (int p = 0; p < 8; ++p) {
-      f[p] = block_pair<S>(v, p);
-      m = max_nan(m, max_nan(fabsf(f[p].x), fabsf(f[p].y)));
-      f[p] = mul2(f[p], splat(lift));
-    }
-    const bool special = !(m <= 3.402823466e38f);
-    const uint32_t sc = special ? 0x7fu : exact_scale(m * lift, big, r448);
-    const float s = special ? 0.0f : e4m3_value(sc);
-    const float inv = s > 0.0f ? s_enc / s : 0.0f;
-    uint32_t q[2] = {0u, 0u};
-    if (!special) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        float2 up[4], down[4];
-#pragma unroll
-        for (int p = 0; p < 4; ++p) {
-          const float2 w = mul2(f[4 * h + p], splat(inv));
-          up[p] = mul2(w, splat(kUp));
-          down[p] = mul2(w, splat(kDown));
-        }
-        const uint32_t hi = e2m1x8(up);
-        uint32_t lo = e2m1x8(down);
-        if (lo != hi) {
-          const double big_s = static_cast<double>(big) * static_cast<double>(s);
-          uint32_t fixed = 0;
-#pragma unroll
-          for (int p = 0; p < 8; ++p) {
-            const uint32_t cl = (lo >> (4 * p)) & 15u, ch = (hi >> (4 * p)) & 15u;
-            const float m1 = fabsf(p & 1 ? f[4 * h + p / 2].y : f[4 * h + p / 2].x);
-            fixed |= (cl == ch ? cl : (exact_code(m1, big_s, cl & 7u, ch & 7u) | (ch & 8u))) << (4 * p);
-          }
-          lo = fixed;
-        }
-        q[h] = lo;
-      }
-    }
-    st_stream8(a.data + row * a.data_pitch + static_cast<int64_t>(col) * 8, make_uint2(q[0], q[1]));
-    a.scale[row * a.scale_pitch + col] = static_cast<uint8_t>(sc);
+  if (std::is_same<S, Bf16>::value && t.short_big) quantize_blocks<S, true>(a, t, first, step);
+  else quantize_blocks<S, false>(a, t, first, step);
+}
+
+// A small matrix in one launch: a cluster of eight CTAs finds A, exchanges it
+// through shared memory and quantises what it has just read (from L2).
+constexpr int kSmallCtas = 8, kSmallThreads = 1024;
+constexpr int64_t kSmallBlocks = 32768;  // blocks of 16
+template <typename S>
+__global__ void __cluster_dims__(kSmallCtas, 1, 1) __launch_bounds__(kSmallThreads) situ_nvfp4_small_kernel(const StoreArgs a) {
+  __shared__ unsigned int warp_max[kSmallThreads / 32];
+  __shared__ unsigned int cta_max[kSmallCtas];
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * kSmallThreads + threadIdx.x, step = kSmallCtas * kSmallThreads;
+  int64_t row;
+  int64_t col;
+  uint4 v[8 / S::kPairs];
+  float m = 0.0f;
+  for (int64_t i = first; i < a.blocks; i += step) {
+    get_block<S>(a, i, row, col, v);
+    m = fmaxf(m, block_finite_max<S>(v));
   }
+  const unsigned int bits = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
+  if ((threadIdx.x & 31) == 0) warp_max[threadIdx.x >> 5] = bits;
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    const unsigned int most = __reduce_max_sync(0xffffffffu, warp_max[threadIdx.x]);
+    if (threadIdx.x < kSmallCtas)  // into slot `rank` of CTA threadIdx.x
+      asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(peer_addr(&cta_max[cluster_rank()], threadIdx.x)), "r"(most)
+                   : "memory");
+  }
+  cluster_sync();
+  unsigned int most = 0;
+#pragma unroll
+  for (int c = 0; c < kSmallCtas; ++c) most = max(most, cta_max[c]);
+  const float amax = __uint_as_float(most);
+  if (first == 0) *reinterpret_cast<float*>(a.amax_out) = amax;
+  const TensorScale t(amax);
+  if (std::is_same<S, Bf16>::value && t.short_big) quantize_blocks<S, true>(a, t, first, step);
+  else quantize_blocks<S, false>(a, t, first, step);
 }
 
 // Two E2M1 codes as an exact half2.
@@ -199,15 +355,15 @@ __global__ void __launch_bounds__(kStoreThreads) situ_nvfp4_dequantize_kernel(co
   const int64_t step = static_cast<int64_t>(gridDim.x) * kStoreThreads;
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * kStoreThreads + threadIdx.x; i < a.blocks; i += step) {
     int64_t row;
-    uint32_t col;
+    int64_t col;
     block_at(a, i, row, col);
-    const uint2 q = ld_stream8(a.data + row * a.data_pitch + static_cast<int64_t>(col) * 8);
+    const uint2 q = ld_stream8(a.data + row * a.data_pitch + col * 8);
     const float s = static_cast<float>(unit * static_cast<double>(e4m3_value(a.scale[row * a.scale_pitch + col])));
     uint4 o[8 / S::kPairs];
 #pragma unroll
     for (int p = 0; p < 8; ++p)
       S::put(o[p / S::kPairs], p % S::kPairs, mul2(e2m1_pair(((p < 4 ? q.x : q.y) >> (8 * (p & 3))) & 0xffu), splat(s)));
-    char* out = a.out + row * a.out_pitch + static_cast<int64_t>(col) * (8 / S::kPairs * kVecBytes);
+    char* out = a.out + row * a.out_pitch + col * (8 / S::kPairs * kVecBytes);
 #pragma unroll
     for (int k = 0; k < 8 / S::kPairs; k += 2) {
       if (a.wide) {
@@ -1136,10 +1292,11 @@ situ_status_t store_check(situ_dtype_t dtype, int64_t rows, int64_t cols, int64_
   return SITU_OK;
 }
 
-void fill_store(StoreArgs* a, int64_t rows, int64_t cols) {
+void fill_store(StoreArgs* a, int64_t rows, int64_t cols, bool flat) {
   a->rows = rows;
   a->per_row = static_cast<uint32_t>(cols / 16);
   a->blocks = rows * (cols / 16);
+  a->flat = flat;
 }
 
 // Whether every vector pair of a matrix is 32-byte aligned.
@@ -1183,7 +1340,9 @@ situ_status_t situ_glu_nvfp4_quantize(const void* x, situ_dtype_t dtype, int64_t
         if (overlap(outs[i], outs[k])) return fail(SITU_ERR_INVALID_ARG, "outputs overlap each other");
     }
   }
-  if (amax_given != 1) {
+  const bool bf = dtype == SITU_DTYPE_BF16;
+  const bool small = amax_given == 0 && rows > 0 && rows <= kSmallBlocks / (cols / 16);
+  if (amax_given != 1 && !small) {
     cudaError_t err = cudaMemsetAsync(amax, 0, sizeof(float), s);
     if (err != cudaSuccess) return fail(SITU_ERR_CUDA, "cudaMemsetAsync: %s", cudaGetErrorString(err));
   }
@@ -1198,8 +1357,14 @@ situ_status_t situ_glu_nvfp4_quantize(const void* x, situ_dtype_t dtype, int64_t
   a.amax = amax;
   a.amax_out = reinterpret_cast<unsigned int*>(amax);
   a.wide = wide_rows(x, a.x_pitch);
-  fill_store(&a, rows, cols);
-  const bool bf = dtype == SITU_DTYPE_BF16;
+  fill_store(&a, rows, cols,
+             rows == 1 || (x_row_stride == cols &&
+                           (only || (data_row_stride == cols / 2 && scale_row_stride == cols / 16))));
+  if (small) {
+    auto k = bf ? situ_nvfp4_small_kernel<Bf16> : situ_nvfp4_small_kernel<F32>;
+    k<<<kSmallCtas, kSmallThreads, 0, s>>>(a);
+    return check_launch("situ_glu_nvfp4_quantize (one launch)");
+  }
   const int64_t ctas = (a.blocks + kStoreThreads - 1) / kStoreThreads;
   int grid = 0;
   if (amax_given != 1) {
@@ -1247,7 +1412,8 @@ situ_status_t situ_glu_nvfp4_dequantize(const void* data, int64_t data_row_strid
   a.out = static_cast<char*>(out);
   a.out_pitch = out_row_stride * es;
   a.wide = wide_rows(out, a.out_pitch);
-  fill_store(&a, rows, cols);
+  fill_store(&a, rows, cols,
+             rows == 1 || (out_row_stride == cols && data_row_stride == cols / 2 && scale_row_stride == cols / 16));
   auto k = dtype == SITU_DTYPE_BF16 ? situ_nvfp4_dequantize_kernel<Bf16> : situ_nvfp4_dequantize_kernel<F32>;
   int grid = 0;
   st = launch_grid(reinterpret_cast<const void*>(k), kStoreThreads, 0, (a.blocks + kStoreThreads - 1) / kStoreThreads,
