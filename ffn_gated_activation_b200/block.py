@@ -52,39 +52,50 @@ class _Scope:
 
 
 def _cuda(t: torch.Tensor, what: str) -> torch.device:
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{what} must be a CUDA tensor")
     return t.device
 
 
-def _same_device(device, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} must be on {device}, got {t.device}")
+def _on(t: torch.Tensor, device, what: str) -> None:
+    if t.device != device:
+        raise ValueError(f"{what} must be on {device}, got {t.device}")
 
 
-def _matrix(t: torch.Tensor, cols: int) -> torch.Tensor:
+def _matrix(t: torch.Tensor, cols: int):
     """[..., cols] as [rows, cols] with each row's elements adjacent and rows
-    not overlapping (copied where they are not)."""
-    if t.dim() == 2 and t.is_contiguous():
-        return t
-    t2 = t if t.dim() == 2 else t.reshape(-1, cols)
-    if t2.numel() and (t2.stride(1) != 1 or (t2.shape[0] > 1 and t2.stride(0) < cols)):
-        t2 = t2.contiguous()
-    return t2
-
-
-def _pitch(t2: torch.Tensor) -> int:
-    return t2.stride(0) if t2.shape[0] > 1 else t2.shape[1]
-
-
-def _ptr(t):
-    return t.data_ptr() if t is not None else None
+    not overlapping (copied where they are not), and its row pitch."""
+    if t.dim() != 2:
+        t = t.reshape(-1, cols)
+    if t.is_contiguous():
+        return t, cols
+    rows = t.shape[0]
+    if t.numel() and (t.stride(1) != 1 or (rows > 1 and t.stride(0) < cols)):
+        return t.contiguous(), cols
+    return t, t.stride(0) if rows > 1 else cols
 
 
 def _check_eps(eps):
     if not (isinstance(eps, (int, float)) and math.isfinite(eps) and eps >= 0):
         raise ValueError(f"eps must be a finite number >= 0, got {eps!r}")
+
+
+def _out(out, shape, dtype, device, what):
+    """A matrix output, allocated when not given: (tensor, its 2-D view, row pitch)."""
+    cols = shape[-1]
+    if out is None:
+        out = torch.empty(shape, dtype=dtype, device=device)
+        return out, out, cols  # contiguous: its rows follow from the pointer and the pitch
+    o2 = _given(out, tuple(shape), device, what, dtype)
+    return out, o2, o2.stride(0) if o2.shape[0] > 1 else cols
+
+
+def _out_like(out, x, cols, what):
+    """_out for an output of x's shape and dtype."""
+    if out is None and x.is_contiguous():
+        out = torch.empty_like(x)
+        return out, out, cols
+    return _out(out, x.shape, x.dtype, x.device, what)
 
 
 # ---- residual addition + RMS norm -------------------------------------------------
@@ -93,26 +104,20 @@ def _norm_args(x, weight, eps, residual):
     """Checks of a norm's inputs; returns (device, dtype code, weight dtype code, hidden)."""
     device = _cuda(x, "x")
     _check_eps(eps)
-    if x.dim() < 1:
+    shape = x.shape
+    if not shape:
         raise ValueError("x must be [..., hidden]")
-    hidden = x.shape[-1]
-    dtype = _dtype_code(x, "x")
-    wdtype = _dtype_code(weight, "weight")
+    hidden = shape[-1]
+    dtype, wdtype = _dtype_code(x, "x"), _dtype_code(weight, "weight")
     if weight.dim() != 1 or weight.shape[0] != hidden:
         raise ValueError(f"weight must be [{hidden}], got {tuple(weight.shape)}")
-    _same_device(device, weight=weight, residual=residual)
-    if residual is not None and (residual.shape != x.shape or residual.dtype != x.dtype):
-        raise ValueError(f"residual must have x's shape {tuple(x.shape)} and dtype {x.dtype}, got "
-                         f"{tuple(residual.shape)} {residual.dtype}")
+    _on(weight, device, "weight")
+    if residual is not None:
+        if residual.shape != shape or residual.dtype != x.dtype:
+            raise ValueError(f"residual must have x's shape {tuple(shape)} and dtype {x.dtype}, got "
+                             f"{tuple(residual.shape)} {residual.dtype}")
+        _on(residual, device, "residual")
     return device, dtype, wdtype, hidden
-
-
-def _like(out, x, what):
-    """An output of x's shape and dtype, allocated when not given; (tensor, 2-D view)."""
-    if out is None:
-        out = torch.empty_like(x, memory_format=torch.contiguous_format)
-        return out, out if x.dim() == 2 else out.view(-1, x.shape[-1])
-    return out, _given(out, tuple(x.shape), x.device, what, x.dtype)
 
 
 def situ_glu_rms_norm_fwd(x: torch.Tensor, weight: torch.Tensor, eps: float = DEFAULT_EPSILON,
@@ -125,16 +130,18 @@ def situ_glu_rms_norm_fwd(x: torch.Tensor, weight: torch.Tensor, eps: float = DE
     if residual is None and h_out is not None:
         raise ValueError("h_out needs a residual")
     with _Scope(device, stream) as handle:
-        x2, w, h, h2 = _matrix(x, hidden), weight.contiguous(), None, None
-        y, y2 = _like(out, x, "out")
-        r2 = None
+        x2, xp = _matrix(x, hidden)
+        w = weight.contiguous()
+        y, y2, yp = _out_like(out, x, hidden, "out")
+        h, r_ptr, rp, h_ptr, hp = None, None, 0, None, 0
         if residual is not None:
-            r2 = _matrix(residual, hidden)
-            h, h2 = _like(h_out, x, "h_out")
-        st = abi.situ_glu_rms_norm_fwd(x2.data_ptr(), dtype, x2.shape[0], hidden, _pitch(x2), _ptr(r2),
-                                       _pitch(r2) if r2 is not None else 0, w.data_ptr(), wdtype, float(eps), _ptr(h2),
-                                       _pitch(h2) if h2 is not None else 0, y2.data_ptr(), _pitch(y2), handle)
-    abi.check(st, "situ_glu_rms_norm_fwd")
+            r2, rp = _matrix(residual, hidden)
+            h, h2, hp = _out_like(h_out, x, hidden, "h_out")
+            r_ptr, h_ptr = r2.data_ptr(), h2.data_ptr()
+        st = abi.situ_glu_rms_norm_fwd(x2.data_ptr(), dtype, x2.shape[0], hidden, xp, r_ptr, rp, w.data_ptr(), wdtype, eps,
+                                       h_ptr, hp, y2.data_ptr(), yp, handle)
+    if st:
+        abi.check(st, "situ_glu_rms_norm_fwd")
     return y, h
 
 
@@ -150,17 +157,21 @@ def situ_glu_rms_norm_fwd_mxfp8(x: torch.Tensor, weight: torch.Tensor, eps: floa
     if hidden % 32:
         raise ValueError(f"hidden must be a multiple of 32, got {hidden}")
     with _Scope(device, stream) as handle:
-        x2, w, h, h2 = _matrix(x, hidden), weight.contiguous(), None, None
+        x2, xp = _matrix(x, hidden)
+        w = weight.contiguous()
         data, scale, d2, s2 = _mx_buffers(tuple(x.shape[:-1]), hidden, device, data, scale)
-        r2 = None
+        h, r_ptr, rp, h_ptr, hp = None, None, 0, None, 0
         if residual is not None:
-            r2 = _matrix(residual, hidden)
-            h, h2 = _like(h_out, x, "h_out")
-        st = abi.situ_glu_rms_norm_fwd_mxfp8(x2.data_ptr(), dtype, x2.shape[0], hidden, _pitch(x2), _ptr(r2),
-                                             _pitch(r2) if r2 is not None else 0, w.data_ptr(), wdtype, float(eps),
-                                             _ptr(h2), _pitch(h2) if h2 is not None else 0, d2.data_ptr(), _pitch(d2),
-                                             s2.data_ptr(), _pitch(s2), _mx_rule(rule), handle)
-    abi.check(st, "situ_glu_rms_norm_fwd_mxfp8")
+            r2, rp = _matrix(residual, hidden)
+            h, h2, hp = _out_like(h_out, x, hidden, "h_out")
+            r_ptr, h_ptr = r2.data_ptr(), h2.data_ptr()
+        rows = x2.shape[0]
+        st = abi.situ_glu_rms_norm_fwd_mxfp8(x2.data_ptr(), dtype, rows, hidden, xp, r_ptr, rp, w.data_ptr(), wdtype, eps,
+                                             h_ptr, hp, d2.data_ptr(), d2.stride(0) if rows > 1 else hidden,
+                                             s2.data_ptr(), s2.stride(0) if rows > 1 else hidden // 32, _mx_rule(rule),
+                                             handle)
+    if st:
+        abi.check(st, "situ_glu_rms_norm_fwd_mxfp8")
     return data, scale, h
 
 
@@ -171,33 +182,45 @@ def situ_glu_rms_norm_bwd(grad_y: torch.Tensor, h: torch.Tensor, weight: torch.T
     """Gradients of the forward from its h (x where there was no residual):
     returns (d_x, d_weight or None).  d_x is the gradient of x and of the
     residual; ``grad_h`` is the gradient that reaches h by itself (the residual
-    stream's).  d_weight is summed in fp32 in an order that the shape fixes."""
+    stream's).  d_weight is summed in fp32 in an order that the shape fixes.
+    Calls that overlap on the GPU need a ``workspace`` each
+    (situ_glu_rms_norm_bwd_workspace_bytes; allocated when not given)."""
     device, dtype, wdtype, hidden = _norm_args(h, weight, eps, None)
     for name, g in (("grad_y", grad_y), ("grad_h", grad_h)):
-        if g is not None and (g.shape != h.shape or g.dtype != h.dtype):
-            raise ValueError(f"{name} must have h's shape {tuple(h.shape)} and dtype {h.dtype}, got "
-                             f"{tuple(g.shape)} {g.dtype}")
-    _same_device(device, grad_y=grad_y, grad_h=grad_h)
+        if g is not None:
+            if g.shape != h.shape or g.dtype != h.dtype:
+                raise ValueError(f"{name} must have h's shape {tuple(h.shape)} and dtype {h.dtype}, got "
+                                 f"{tuple(g.shape)} {g.dtype}")
+            _on(g, device, name)
     with _Scope(device, stream) as handle:
-        h2, g2, w = _matrix(h, hidden), _matrix(grad_y, hidden), weight.contiguous()
-        gh2 = _matrix(grad_h, hidden) if grad_h is not None else None
-        d_x, dx2 = _like(d_x, h, "d_x")
+        h2, hp = _matrix(h, hidden)
+        g2, gp = _matrix(grad_y, hidden)
+        w = weight.contiguous()
+        gh_ptr, ghp = None, 0
+        if grad_h is not None:
+            gh2, ghp = _matrix(grad_h, hidden)
+            gh_ptr = gh2.data_ptr()
+        d_x, dx2, dxp = _out_like(d_x, h, hidden, "d_x")
+        dw_ptr = None
         if not want_dw:
             d_weight = None
-        elif d_weight is None:
-            d_weight = torch.empty(hidden, dtype=weight.dtype, device=device)
-        elif tuple(d_weight.shape) != (hidden,) or d_weight.dtype != weight.dtype or d_weight.device != device or \
-                not d_weight.is_contiguous():
-            raise ValueError(f"d_weight must be a contiguous {weight.dtype} [{hidden}] on {device}")
+        else:
+            if d_weight is None:
+                d_weight = torch.empty(hidden, dtype=weight.dtype, device=device)
+            elif tuple(d_weight.shape) != (hidden,) or d_weight.dtype != weight.dtype or d_weight.device != device or \
+                    not d_weight.is_contiguous():
+                raise ValueError(f"d_weight must be a contiguous {weight.dtype} [{hidden}] on {device}")
+            dw_ptr = d_weight.data_ptr()
         tokens = h2.shape[0]
-        ws = abi.situ_glu_rms_norm_bwd_workspace_bytes(tokens, hidden, int(want_dw))
+        ws = abi.situ_glu_rms_norm_bwd_workspace_bytes(tokens, hidden, 1) if want_dw else 0
+        ws_ptr = None
         if ws:
             workspace = _workspace(workspace, ws, device)
-        st = abi.situ_glu_rms_norm_bwd(g2.data_ptr(), _pitch(g2), _ptr(gh2), _pitch(gh2) if gh2 is not None else 0,
-                                       h2.data_ptr(), dtype, tokens, hidden, _pitch(h2), w.data_ptr(), wdtype, float(eps),
-                                       dx2.data_ptr(), _pitch(dx2), _ptr(d_weight), _ptr(workspace) if ws else None, ws,
-                                       handle)
-    abi.check(st, "situ_glu_rms_norm_bwd")
+            ws_ptr = workspace.data_ptr()
+        st = abi.situ_glu_rms_norm_bwd(g2.data_ptr(), gp, gh_ptr, ghp, h2.data_ptr(), dtype, tokens, hidden, hp,
+                                       w.data_ptr(), wdtype, eps, dx2.data_ptr(), dxp, dw_ptr, ws_ptr, ws, handle)
+    if st:
+        abi.check(st, "situ_glu_rms_norm_bwd")
     return d_x, d_weight
 
 
@@ -272,26 +295,33 @@ def situ_glu_moe_fwd(x: torch.Tensor, topk_ids: torch.Tensor, topk_weights: torc
     experts, inter = w2.shape[0], w2.shape[2]
     if topk_weights is not None and topk_weights.shape != topk_ids.shape:
         raise ValueError(f"topk_weights must be {tuple(topk_ids.shape)}, got {tuple(topk_weights.shape)}")
-    _same_device(device, topk_ids=topk_ids, topk_weights=topk_weights, w1=w1, w2=w2)
-    wdtype = _dtype_code(topk_weights, "topk_weights") if topk_weights is not None else abi.SITU_DTYPE_F32
+    for t, name in ((topk_ids, "topk_ids"), (w1, "w1"), (w2, "w2")):
+        _on(t, device, name)
+    wdtype = abi.SITU_DTYPE_F32
+    if topk_weights is not None:
+        _on(topk_weights, device, "topk_weights")
+        wdtype = _dtype_code(topk_weights, "topk_weights")
     with _Scope(device, stream) as handle:
-        x2, ids = _matrix(x, hidden), _matrix(topk_ids, topk)
-        tw = _matrix(topk_weights, topk) if topk_weights is not None else None
-        w1f, w2f = _matrix(w1, hidden), _matrix(w2, inter)
-        if out is None:
-            out = torch.empty(tokens, hidden, dtype=torch.bfloat16, device=device)
-            o2 = out
-        else:
-            o2 = _given(out, (tokens, hidden), device, "out", torch.bfloat16)
+        x2, xp = _matrix(x, hidden)
+        ids, idp = _matrix(topk_ids, topk)
+        tw_ptr, twp = None, topk
+        if topk_weights is not None:
+            tw, twp = _matrix(topk_weights, topk)
+            tw_ptr = tw.data_ptr()
+        w1f, w1p = _matrix(w1, hidden)
+        w2f, w2p = _matrix(w2, inter)
+        out, o2, op = _out(out, (tokens, hidden), torch.bfloat16, device, "out")
         ws = abi.situ_glu_moe_workspace_bytes(tokens, topk, hidden, inter)
+        ws_ptr = None
         if ws:
             workspace = _workspace(workspace, ws, device)
-        st = abi.situ_glu_moe_fwd(x2.data_ptr(), tokens, hidden, _pitch(x2), ids.data_ptr(), topk, _pitch(ids), _ptr(tw),
-                                  wdtype, _pitch(tw) if tw is not None else topk, w1f.data_ptr(), experts, inter,
-                                  _pitch(w1f), w2f.data_ptr(), _pitch(w2f), float(beta), int(linear_beta is not None),
-                                  float(linear_beta) if linear_beta is not None else 0.0, o2.data_ptr(), _pitch(o2),
-                                  _ptr(workspace) if ws else None, ws, handle)
-    abi.check(st, "situ_glu_moe_fwd")
+            ws_ptr = workspace.data_ptr()
+        st = abi.situ_glu_moe_fwd(x2.data_ptr(), tokens, hidden, xp, ids.data_ptr(), topk, idp, tw_ptr, wdtype, twp,
+                                  w1f.data_ptr(), experts, inter, w1p, w2f.data_ptr(), w2p, beta,
+                                  int(linear_beta is not None), linear_beta if linear_beta is not None else 0.0,
+                                  o2.data_ptr(), op, ws_ptr, ws, handle)
+    if st:
+        abi.check(st, "situ_glu_moe_fwd")
     return out
 
 
@@ -318,24 +348,28 @@ def situ_glu_nvfp4_quantize(x: torch.Tensor, amax: torch.Tensor | None = None, d
     if amax_only and amax is not None:
         raise ValueError("amax_only computes the tensor maximum: do not pass one")
     with _Scope(device, stream) as handle:
-        x2, d2, s2 = _matrix(x, cols), None, None
+        x2, xp = _matrix(x, cols)
+        d_ptr, dp, s_ptr, sp = None, cols // 2, None, cols // 16
         if not amax_only:
-            if data is None:
-                data = torch.empty(lead + (cols // 2,), dtype=torch.uint8, device=device)
-            d2 = _given(data, lead + (cols // 2,), device, "NVFP4 data")
-            if scale is None:
-                scale = torch.empty(lead + (cols // 16,), dtype=torch.float8_e4m3fn, device=device)
-            s2 = _given(scale, lead + (cols // 16,), device, "NVFP4 scale")
-        given = amax is not None
+            data, d2, dp = _bytes(data, lead + (cols // 2,), torch.uint8, device, "NVFP4 data")
+            scale, s2, sp = _bytes(scale, lead + (cols // 16,), torch.float8_e4m3fn, device, "NVFP4 scale")
+            d_ptr, s_ptr = d2.data_ptr(), s2.data_ptr()
+        given = 2 if amax_only else int(amax is not None)
         if amax is None:
             amax = amax_out if amax_out is not None else torch.empty(1, dtype=torch.float32, device=device)
         _amax_word(amax, device)
-        st = abi.situ_glu_nvfp4_quantize(x2.data_ptr(), dtype, x2.shape[0], cols, _pitch(x2), _ptr(d2),
-                                         _pitch(d2) if d2 is not None else cols // 2, _ptr(s2),
-                                         _pitch(s2) if s2 is not None else cols // 16, amax.data_ptr(),
-                                         2 if amax_only else int(given), handle)
-    abi.check(st, "situ_glu_nvfp4_quantize")
+        st = abi.situ_glu_nvfp4_quantize(x2.data_ptr(), dtype, x2.shape[0], cols, xp, d_ptr, dp, s_ptr, sp, amax.data_ptr(),
+                                         given, handle)
+    if st:
+        abi.check(st, "situ_glu_nvfp4_quantize")
     return (None, None, amax) if amax_only else (data, scale, amax)
+
+
+def _bytes(given, shape, dtype, device, what):
+    """As _out for codes or scales: one byte an element, of any dtype where given."""
+    if given is None:
+        return _out(None, shape, dtype, device, what)
+    return (given,) + _out(given, shape, given.dtype if given.element_size() == 1 else None, device, what)[1:]
 
 
 def _codes(data, scale, what):
@@ -354,17 +388,16 @@ def situ_glu_nvfp4_dequantize(data: torch.Tensor, scale: torch.Tensor, amax: tor
     """The values q * scale * amax / 2688 that NVFP4 codes stand for, [..., C] in ``dtype``."""
     device = _cuda(data, "data")
     cols = _codes(data, scale, "situ_glu_nvfp4_dequantize")
-    _same_device(device, scale=scale)
+    _on(scale, device, "scale")
     _amax_word(amax, device)
-    shape = tuple(data.shape[:-1]) + (cols,)
     with _Scope(device, stream) as handle:
-        d2, s2 = _matrix(data, cols // 2), _matrix(scale, cols // 16)
-        if out is None:
-            out = torch.empty(shape, dtype=dtype, device=device)
-        o2 = _given(out, shape, device, "out", dtype)
-        st = abi.situ_glu_nvfp4_dequantize(d2.data_ptr(), _pitch(d2), s2.data_ptr(), _pitch(s2), amax.data_ptr(),
-                                           d2.shape[0], cols, o2.data_ptr(), _dtype_code(out, "out"), _pitch(o2), handle)
-    abi.check(st, "situ_glu_nvfp4_dequantize")
+        d2, dp = _matrix(data, cols // 2)
+        s2, sp = _matrix(scale, cols // 16)
+        out, o2, op = _out(out, tuple(data.shape[:-1]) + (cols,), dtype, device, "out")
+        st = abi.situ_glu_nvfp4_dequantize(d2.data_ptr(), dp, s2.data_ptr(), sp, amax.data_ptr(), d2.shape[0], cols,
+                                           o2.data_ptr(), _dtype_code(out, "out"), op, handle)
+    if st:
+        abi.check(st, "situ_glu_nvfp4_dequantize")
     return out
 
 
@@ -385,28 +418,29 @@ def situ_glu_nvfp4_gemm(a, w, offsets: torch.Tensor | None = None, out_dtype: to
     if _codes(wd, wsc, "w") != k or ad.dim() != 2 or wd.dim() not in (2, 3):
         raise ValueError(f"a must hold [T, K] and w [E, N, K] or [N, K], got codes {tuple(ad.shape)} and {tuple(wd.shape)}")
     experts, n = (wd.shape[0], wd.shape[1]) if wd.dim() == 3 else (1, wd.shape[0])
-    _same_device(device, a_scale=asc, w_data=wd, w_scale=wsc, w_amax=wa, offsets=offsets)
+    for t, name in ((asc, "a's scales"), (wd, "w's codes"), (wsc, "w's scales"), (wa, "w's amax")):
+        _on(t, device, name)
     _amax_word(aa, device, "a's amax")
     if wa.dtype != torch.float32 or wa.numel() not in (1, experts):
         raise ValueError(f"w's amax must be 1 or {experts} float32 elements")
     if offsets is None:
         if experts != 1:
             raise ValueError(f"offsets are needed with {experts} experts")
-    elif offsets.dtype != torch.int64 or offsets.dim() != 1 or offsets.numel() != experts + 1:
-        raise ValueError(f"offsets must be int64 [{experts + 1}]")
+    elif offsets.device != device or offsets.dtype != torch.int64 or offsets.dim() != 1 or offsets.numel() != experts + 1:
+        raise ValueError(f"offsets must be int64 [{experts + 1}] on {device}")
     if out_dtype not in (torch.bfloat16, torch.float32):
         raise TypeError(f"out_dtype must be bfloat16 or float32, got {out_dtype}")
     tokens = ad.shape[0]
     with _Scope(device, stream) as handle:
-        ad, asc = _matrix(ad, k // 2), _matrix(asc, k // 16)
-        wd, wsc, wa = _matrix(wd, k // 2), _matrix(wsc, k // 16), wa.reshape(-1).contiguous()
+        (ad, adp), (asc, asp) = _matrix(ad, k // 2), _matrix(asc, k // 16)
+        (wd, wdp), (wsc, wsp) = _matrix(wd, k // 2), _matrix(wsc, k // 16)
+        wa = wa.reshape(-1).contiguous()
         off = offsets.contiguous() if offsets is not None else None
-        if out is None:
-            out = torch.empty(tokens, n, dtype=out_dtype, device=device)
-        o2 = _given(out, (tokens, n), device, "out", out_dtype)
-        st = abi.situ_glu_nvfp4_gemm(ad.data_ptr(), _pitch(ad), asc.data_ptr(), _pitch(asc), aa.data_ptr(), tokens, k,
-                                     wd.data_ptr(), _pitch(wd), wsc.data_ptr(), _pitch(wsc), wa.data_ptr(),
-                                     0 if wa.numel() == 1 else 1, experts, n, _ptr(off), o2.data_ptr(),
-                                     _dtype_code(out, "out"), _pitch(o2), handle)
-    abi.check(st, "situ_glu_nvfp4_gemm")
+        out, o2, op = _out(out, (tokens, n), out_dtype, device, "out")
+        st = abi.situ_glu_nvfp4_gemm(ad.data_ptr(), adp, asc.data_ptr(), asp, aa.data_ptr(), tokens, k, wd.data_ptr(), wdp,
+                                     wsc.data_ptr(), wsp, wa.data_ptr(), 0 if wa.numel() == 1 else 1, experts, n,
+                                     off.data_ptr() if off is not None else None, o2.data_ptr(), _dtype_code(out, "out"),
+                                     op, handle)
+    if st:
+        abi.check(st, "situ_glu_nvfp4_gemm")
     return out

@@ -130,8 +130,20 @@ def test_host_tensors_are_refused(call):
 
 def test_matrix_views_are_copied_only_where_rows_are_not_runs():
     t = torch.arange(48.0).reshape(4, 12)
-    assert block._matrix(t[:, 2:8], 6).data_ptr() == t[:, 2:8].data_ptr()
-    assert block._matrix(t.t(), 4).is_contiguous()
-    assert block._matrix(t[:1].expand(4, 12), 12).stride(0) == 12  # overlapping rows
-    assert block._matrix(t[:0], 12).shape == (0, 12)
-    assert block._matrix(torch.zeros(2, 3, 12), 12).shape == (6, 12)
+    m, pitch = block._matrix(t[:, 2:8], 6)
+    assert m.data_ptr() == t[:, 2:8].data_ptr() and pitch == 12
+    assert block._matrix(t.t(), 4)[0].is_contiguous()
+    m, pitch = block._matrix(t[:1].expand(4, 12), 12)  # overlapping rows
+    assert m.stride(0) == 12 and pitch == 12
+    assert block._matrix(t[:0], 12)[0].shape == (0, 12)
+    assert block._matrix(torch.zeros(2, 3, 12), 12)[0].shape == (6, 12)
+    assert block._matrix(t[1:2, 3:9], 6)[1] == 6  # one row: its pitch is its width
+
+
+def test_outputs_of_the_wrong_shape_are_refused():
+    with pytest.raises(ValueError, match="shape"):
+        block._out(torch.empty(3, 4), (3, 5), torch.float32, torch.device("cpu"), "out")
+    with pytest.raises(TypeError, match="one-byte"):
+        block._bytes(torch.empty(3, 4), (3, 4), torch.uint8, torch.device("cpu"), "codes")
+    o, o2, pitch = block._out(torch.empty(3, 9)[:, :4], (3, 4), torch.float32, torch.device("cpu"), "out")
+    assert o2.data_ptr() == o.data_ptr() and pitch == 9

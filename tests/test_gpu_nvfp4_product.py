@@ -108,9 +108,12 @@ def test_borders_between_codes(dtype, cuda_device):
         check_codes(x, data, scale, given.cpu(), f"amax {amax}")
 
 
-def test_given_maxima_that_do_not_fit(cuda_device):
-    x = make(torch.float32, 8, 64, seed=3)
-    for a in (0.0, 0.25, 1e-40, float("inf"), float("nan")):
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_given_maxima_that_do_not_fit(dtype, cuda_device):
+    """Others than the matrix' own: none, too small, with 24 bits, tiny, not finite."""
+    x = make(dtype, 8, 64, seed=3)
+    x[1] *= 1e-38 if dtype == torch.float32 else 1e-30
+    for a in (0.0, 0.25, 3.4000001, 7.7777, 1e-40, 1e-37, 1e37, float("inf"), float("nan")):
         given = torch.tensor([a], device=cuda_device)
         data, scale, _ = pkg.situ_glu_nvfp4_quantize(x.to(cuda_device), amax=given)
         check_codes(x, data, scale, given.cpu(), f"amax {a}")
