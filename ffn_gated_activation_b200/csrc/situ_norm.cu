@@ -18,9 +18,9 @@
 namespace {
 
 constexpr int64_t kNormMaxRowBytes = 65536;  // eight vectors in each of 512 threads
-// Threads of a CTA with V vectors a thread (row_shape below).
-template <int V>
-constexpr int kNormThreads = V == 8 ? 512 : 256;
+// The most threads of a CTA with V vectors a thread (row_shape below).
+template <int V, bool MX = false>
+constexpr int kNormThreads = V == 8 || (MX && V == 2) ? 512 : 256;
 
 struct NormArgs {
   const char* x;
@@ -105,7 +105,7 @@ __device__ __forceinline__ uint4 add_vec(const uint4& x, const uint4& r) {
 }
 
 template <typename S, int V, bool RES, bool MX>
-__global__ void __launch_bounds__(kNormThreads<V>) situ_rms_norm_fwd_kernel(const NormArgs a, const MxOut m) {
+__global__ void __launch_bounds__(kNormThreads<V, MX>) situ_rms_norm_fwd_kernel(const NormArgs a, const MxOut m) {
   __shared__ float slots[2][32];
   const int nt = blockDim.x, warps = nt >> 5;
   int flip = 0;
@@ -209,6 +209,9 @@ __global__ void __launch_bounds__(kNormThreads<V>) situ_rms_norm_bwd_kernel(cons
   // The thread's own columns' sums: registers, or (rows of eight vectors a
   // thread, whose sums would spill) the thread's words of shared memory.
   constexpr bool kInSmem = V == 8;
+  // grad_h is loaded with the row (bf16 65536 x 1024: 92 us; loaded after the sums,
+  // 133 us), but for eight vectors, which would spill.
+  constexpr bool kEarly = V < 8;
   extern __shared__ float2 dw_smem[];
   float2 dw_reg[kInSmem ? 1 : V][S::kPairs];
   auto dw = [&](int i, int p) -> float2& {
@@ -222,11 +225,12 @@ __global__ void __launch_bounds__(kNormThreads<V>) situ_rms_norm_bwd_kernel(cons
 #pragma unroll
       for (int p = 0; p < S::kPairs; ++p) dw(i, p) = make_float2(0.0f, 0.0f);
     for (int64_t row = c; row < a.tokens; row += a.chunks) {
-      uint4 h[V], g[V];
+      uint4 h[V], g[V], gh[kEarly ? V : 1];
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         const int j = threadIdx.x + i * nt;
         if (j < a.vpr) {
+          if (kEarly && a.gh != nullptr) gh[i] = ld_stream(a.gh + row * a.gh_pitch + static_cast<int64_t>(j) * kVecBytes);
           h[i] = ld_stream(a.h + row * a.h_pitch + static_cast<int64_t>(j) * kVecBytes);
           g[i] = ld_stream(a.gy + row * a.gy_pitch + static_cast<int64_t>(j) * kVecBytes);
         }
@@ -254,8 +258,9 @@ __global__ void __launch_bounds__(kNormThreads<V>) situ_rms_norm_bwd_kernel(cons
       for (int i = 0; i < V; ++i) {
         const int j = threadIdx.x + i * nt;
         if (j < a.vpr) {
-          uint4 o, gh;
-          if (a.gh != nullptr) gh = ld_stream(a.gh + row * a.gh_pitch + static_cast<int64_t>(j) * kVecBytes);
+          uint4 o;
+          if (!kEarly && a.gh != nullptr) gh[0] = ld_stream(a.gh + row * a.gh_pitch + static_cast<int64_t>(j) * kVecBytes);
+          const uint4& ghi = gh[kEarly ? i : 0];
           float2 w[S::kPairs];
           norm_weights<S>(a.w, a.w_bf16, j, w);
 #pragma unroll
@@ -263,7 +268,7 @@ __global__ void __launch_bounds__(kNormThreads<V>) situ_rms_norm_bwd_kernel(cons
             const float2 f = as_f2(S::pair(h[i], p));
             const float2 gq = mul2(as_f2(S::pair(g[i], p)), splat(q));
             float2 d = fma2(gq, w[p], mul2(f, splat(along)));
-            if (a.gh != nullptr) d = add2(d, as_f2(S::pair(gh, p)));
+            if (a.gh != nullptr) d = add2(d, as_f2(S::pair(ghi, p)));
             S::put(o, p, d);
             dw(i, p) = fma2(gq, f, dw(i, p));
           }
@@ -337,9 +342,9 @@ __global__ void __launch_bounds__(544) situ_rms_norm_bwd_ring_kernel(const NormB
             phase ^= 1u;
           }
         }
-      if (!ok)  // let the copies land (bounded) before the CTA exits
-        for (int s = 0; s < r.stages; ++s)
-          if (issued & (1u << s)) mbar_wait(&full[s], s < stage ? phase : phase ^ 1u);
+      // the CTA leaves with no copy in flight (a bounded wait, as all are)
+      for (int s = 0; s < r.stages; ++s)
+        if (issued & (1u << s)) mbar_wait(&full[s], s < stage ? phase : phase ^ 1u);
     }
     return;
   }
@@ -446,26 +451,42 @@ __global__ void __launch_bounds__(544) situ_rms_norm_bwd_ring_kernel(const NormB
   }
 }
 
-// d_weight[i] = sum of the chunks' partials: 32 columns a CTA, 32 groups of
-// chunks side by side, the groups in order at the end.  Launched so that it may
-// be resident before the backward ends (its wait below is for the whole grid).
-constexpr int kNormFinGroups = 32;
-__global__ void __launch_bounds__(32 * kNormFinGroups)
+// d_weight[i] = sum of the chunks' partials: COLS columns a CTA, 1024 / COLS groups
+// of chunks side by side, then the groups in order, 32 at a time.  Launched so that
+// it may be resident before the backward ends (its wait below is for the whole
+// grid).
+constexpr int kNormFinThreads = 1024;
+template <int COLS>
+__global__ void __launch_bounds__(kNormFinThreads)
     situ_rms_norm_dw_kernel(const float* partials, int64_t chunks, int hidden, void* d_w, int bf16) {
-  __shared__ float part[kNormFinGroups][32];
-  const int col = blockIdx.x * 32 + threadIdx.x;
+  constexpr int kGroups = kNormFinThreads / COLS, kParts = kGroups / 32;
+  __shared__ float part[kGroups][COLS];
+  const int c0 = threadIdx.x % COLS, grp = threadIdx.x / COLS;
+  const int col = blockIdx.x * COLS + c0;
   float s = 0.0f;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (col < hidden) {
 #pragma unroll 4
-    for (int64_t c = threadIdx.y; c < chunks; c += kNormFinGroups) s += __ldcg(partials + c * hidden + col);
+    for (int64_t c = grp; c < chunks; c += kGroups) s += __ldcg(partials + c * hidden + col);
   }
-  part[threadIdx.y][threadIdx.x] = s;
+  part[grp][c0] = s;
   __syncthreads();
-  if (threadIdx.y == 0 && col < hidden) {
-    float t = 0.0f;
+  float t = 0.0f;
+  if (grp < kParts) {
 #pragma unroll
-    for (int g = 0; g < kNormFinGroups; ++g) t += part[g][threadIdx.x];
+    for (int g = 0; g < 32; ++g) t += part[grp * 32 + g][c0];
+  }
+  if (kParts > 1) {
+    __syncthreads();
+    if (grp < kParts) part[grp][c0] = t;
+    __syncthreads();
+    t = 0.0f;
+    if (grp == 0) {
+#pragma unroll
+      for (int g = 0; g < kParts; ++g) t += part[g][c0];
+    }
+  }
+  if (grp == 0 && col < hidden) {
     if (bf16)
       static_cast<__nv_bfloat16*>(d_w)[col] = __float2bfloat16(t);
     else
@@ -475,13 +496,18 @@ __global__ void __launch_bounds__(32 * kNormFinGroups)
 
 // ---- host ---------------------------------------------------------------------
 
-// Threads and vectors per thread of a row of `vpr` vectors.
+// Threads and vectors per thread of a row of `vpr` vectors.  Up to 128 vectors a
+// row is one warp's, so that no barrier parts its sum from its output; wider rows
+// take a CTA of as few warps as leave two (then four, then eight) vectors a thread.
+// MXFP8 rows, with more arithmetic per vector, keep two up to 1024 vectors (bf16
+// 16384 x 7168, time of the forward: 150 us against 160 us with four; native rows
+// 157 us against 140 us) and one vector is slower (32768 x 2048: 87 us, two 78 us).
 struct RowShape {
   int v, threads, rows;  // rows: rows of one CTA (one warp each)
 };
-RowShape row_shape(int vpr) {
-  if (vpr <= 128) return {vpr <= 32 ? 1 : vpr <= 64 ? 2 : 4, 32, 8};
-  const int v = vpr <= 512 ? 2 : vpr <= 1024 ? 4 : 8;
+RowShape row_shape(int vpr, bool mx) {
+  if (vpr <= 128) return {(vpr + 31) / 32, 32, 8};
+  const int v = vpr <= (mx ? 1024 : 512) ? 2 : vpr <= 1024 ? 4 : 8;
   return {v, ((vpr + v - 1) / v + 31) / 32 * 32, 1};
 }
 
@@ -534,12 +560,13 @@ NormRingKernel pick_norm_ring(int v, bool gh) {
   }
 }
 
-// Launch of the staged backward: one CTA per SM for rows that need 512 threads,
-// two or more for narrower ones, each with its share of the shared memory.
+// Launch of the staged backward: one CTA per SM for rows of more than 256 threads,
+// four for narrower ones, each with its share of the shared memory (bf16 8191 x
+// 4096: 51 us, with two 56 us; 32768 x 1536: 77 us, with two 90 us).
 situ_status_t launch_norm_ring(const NormBwdArgs& a, bool bf, cudaStream_t s) {
   const int v = a.vpr <= 256 ? 1 : a.vpr <= 1024 ? 2 : 4;
   const int nt = ((a.vpr + v - 1) / v + 31) / 32 * 32;
-  const int ctas = nt > 256 ? 1 : nt > 128 ? 2 : 4;
+  const int ctas = nt > 256 ? 1 : 4;
   NormRing r;
   r.stage_bytes = (a.gh != nullptr ? 3 : 2) * a.vpr * kVecBytes;
   r.stages = (208 * 1024 / ctas) / r.stage_bytes;
@@ -550,7 +577,10 @@ situ_status_t launch_norm_ring(const NormBwdArgs& a, bool bf, cudaStream_t s) {
   if (st != SITU_OK) return st;
   int grid = 0;
   st = launch_grid(reinterpret_cast<const void*>(k), nt + 32, smem, a.chunks, &grid);
+  int sms = 0;
+  if (st == SITU_OK) st = device_sm_count(&sms);
   if (st != SITU_OK) return st;
+  if (grid > ctas * sms) grid = ctas * sms;
   k<<<grid, nt + 32, smem, s>>>(a, r);
   return check_launch("situ_glu_rms_norm_bwd");
 }
@@ -561,6 +591,7 @@ NormFwdKernel pick_norm_fwd(int v, bool res) {
   switch (v) {
     case 1: return res ? situ_rms_norm_fwd_kernel<S, 1, true, MX> : situ_rms_norm_fwd_kernel<S, 1, false, MX>;
     case 2: return res ? situ_rms_norm_fwd_kernel<S, 2, true, MX> : situ_rms_norm_fwd_kernel<S, 2, false, MX>;
+    case 3: return res ? situ_rms_norm_fwd_kernel<S, 3, true, MX> : situ_rms_norm_fwd_kernel<S, 3, false, MX>;
     case 4: return res ? situ_rms_norm_fwd_kernel<S, 4, true, MX> : situ_rms_norm_fwd_kernel<S, 4, false, MX>;
     default: return res ? situ_rms_norm_fwd_kernel<S, 8, true, MX> : situ_rms_norm_fwd_kernel<S, 8, false, MX>;
   }
@@ -571,6 +602,7 @@ NormBwdKernel pick_norm_bwd(int v) {
   switch (v) {
     case 1: return situ_rms_norm_bwd_kernel<S, 1>;
     case 2: return situ_rms_norm_bwd_kernel<S, 2>;
+    case 3: return situ_rms_norm_bwd_kernel<S, 3>;
     case 4: return situ_rms_norm_bwd_kernel<S, 4>;
     default: return situ_rms_norm_bwd_kernel<S, 8>;
   }
@@ -644,13 +676,23 @@ situ_status_t norm_fwd_entry(const void* x, situ_dtype_t dtype, int64_t tokens, 
   a.vpr = static_cast<int>(hidden * es / kVecBytes);
   a.eps = static_cast<float>(epsilon);
   a.inv_hidden = static_cast<float>(1.0 / static_cast<double>(hidden));
-  const RowShape rs = row_shape(a.vpr);
+  const RowShape rs = row_shape(a.vpr, mx != nullptr);
   const bool bf = dtype == SITU_DTYPE_BF16;
   NormFwdKernel k = mx != nullptr ? (bf ? pick_norm_fwd<Bf16, true>(rs.v, res) : pick_norm_fwd<F32, true>(rs.v, res))
                                   : (bf ? pick_norm_fwd<Bf16, false>(rs.v, res) : pick_norm_fwd<F32, false>(rs.v, res));
   int grid = 0;
-  st = launch_grid(reinterpret_cast<const void*>(k), rs.threads * rs.rows, 0, (tokens + rs.rows - 1) / rs.rows, &grid);
-  if (st != SITU_OK) return st;
+  const int64_t groups = (tokens + rs.rows - 1) / rs.rows;
+  const int cap = g_max_ctas.load(std::memory_order_relaxed);
+  // Native rows of 128 vectors and more: a CTA per group of rows, whose turnover
+  // overlaps one row's stores with the next one's loads (bf16 16384 x 7168: 140 us, a
+  // loop of resident CTAs 153 us; 65536 x 1024: 82, 93).  Narrower rows and MXFP8
+  // ones do better in the loop (60000 x 256: 19, 22; MXFP8 16384 x 7168: 162, 170).
+  if (mx == nullptr && a.vpr >= 128 && cap <= 0 && groups <= INT32_MAX) {
+    grid = static_cast<int>(groups);
+  } else {
+    st = launch_grid(reinterpret_cast<const void*>(k), rs.threads * rs.rows, 0, groups, &grid);
+    if (st != SITU_OK) return st;
+  }
   k<<<grid, dim3(rs.threads, rs.rows), 0, static_cast<cudaStream_t>(stream)>>>(a, mx != nullptr ? *mx : MxOut{});
   return check_launch(what);
 }
@@ -758,12 +800,14 @@ situ_status_t situ_glu_rms_norm_bwd(const void* grad_y, int64_t grad_y_row_strid
   a.eps = static_cast<float>(epsilon);
   a.inv_hidden = static_cast<float>(1.0 / static_cast<double>(hidden));
   const bool bf = dtype == SITU_DTYPE_BF16;
-  // Staged rows from 129 vectors (narrower rows have a warp each and enough of
-  // them in flight) up to 2048, of which two or more fit in shared memory.
+  // Staged rows from 129 vectors up to 2048, of which two or more fit in shared
+  // memory.  Narrower rows have a warp each and enough of them in flight (bf16 65536 x
+  // 1024: 92 us, staged 96; 40000 x 512: 37, staged 48); wider ones gain from the ring
+  // (32768 x 2048: 97 us, direct 105; 8191 x 4096: 51, direct 60).
   if (a.vpr > 128 && a.vpr <= 2048) {
     st = launch_norm_ring(a, bf, s);
   } else {
-    const RowShape rs = row_shape(a.vpr);
+    const RowShape rs = row_shape(a.vpr, false);
     NormBwdKernel k = bf ? pick_norm_bwd<Bf16>(rs.v) : pick_norm_bwd<F32>(rs.v);
     const int smem = rs.v == 8 ? rs.v * rs.threads * (kVecBytes / es) * 4 : 0;
     if (smem > 48 * 1024) {
@@ -782,14 +826,16 @@ situ_status_t situ_glu_rms_norm_bwd(const void* grad_y, int64_t grad_y_row_strid
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3(static_cast<unsigned>((hidden + 31) / 32));
-  cfg.blockDim = dim3(32, kNormFinGroups);
+  const int cols = hidden <= 1024 ? 8 : 32;
+  cfg.gridDim = dim3(static_cast<unsigned>((hidden + cols - 1) / cols));
+  cfg.blockDim = dim3(kNormFinThreads);
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   const cudaError_t err =
-      cudaLaunchKernelEx(&cfg, situ_rms_norm_dw_kernel, static_cast<const float*>(a.partials), a.chunks,
-                         static_cast<int>(hidden), d_weight, weight_dtype == SITU_DTYPE_BF16 ? 1 : 0);
+      cudaLaunchKernelEx(&cfg, cols == 8 ? situ_rms_norm_dw_kernel<8> : situ_rms_norm_dw_kernel<32>,
+                         static_cast<const float*>(a.partials), a.chunks, static_cast<int>(hidden), d_weight,
+                         weight_dtype == SITU_DTYPE_BF16 ? 1 : 0);
   if (err != cudaSuccess)
     return fail(SITU_ERR_CUDA, "situ_glu_rms_norm_bwd (d_weight) launch: %s", cudaGetErrorString(err));
   return check_launch("situ_glu_rms_norm_bwd (d_weight)");

@@ -9,8 +9,10 @@ half(t) the storage type's (bf16 2^-8, fp32 2^-24), both relative.
     two products: 30 u in all.
   * d_x: the same sums bound each of its terms relative to the terms' sizes, so
     64 u of |grad_h| + |q g| + |h| q^3 mean |g h| covers them.
-  * d_weight: a chain of at most ceil(T / 296) + 37 + 8 additions of terms that
-    are each within 32 u.
+  * d_weight: terms that are each within 32 u.  The rows of one of the C chunks
+    (C = T up to 2368, 592 or 296 by the row's width) are added in order, ceil(T / C)
+    additions; then the chunks in 1024 / 8 groups, ceil(C / 128) + 32 + 4 additions, or
+    in 1024 / 32 groups, ceil(C / 32) + 32.  ceil(T / C) + ceil(C / 32) + 36 covers both.
 """
 import numpy as np
 import pytest
@@ -26,8 +28,8 @@ pytestmark = pytest.mark.gpu
 U = 2.0 ** -24
 HALF = {torch.bfloat16: 2.0 ** -8, torch.float32: U}
 EPS = 1e-5
-# one warp a row with 1, 2 and 4 vectors a lane; a CTA a row with 2, 4 and 8; ragged last vectors
-SHAPES = [(torch.bfloat16, h) for h in (8, 256, 264, 1024, 1032, 4104, 7168, 8192, 8200, 32768)] + \
+# one warp a row with 1 to 4 vectors a lane; a CTA a row with 2, 4 and 8; ragged last vectors
+SHAPES = [(torch.bfloat16, h) for h in (8, 256, 264, 520, 1024, 1032, 4104, 7168, 8192, 8200, 32768)] + \
          [(torch.float32, h) for h in (4, 128, 516, 2052, 8196, 16384)]
 
 
@@ -41,6 +43,12 @@ def close(got, ref, bound, what):
     bad = ~((got - ref).abs() <= bound)
     assert not bad.any(), f"{what}: {int(bad.sum())} of {bad.numel()}, first at {bad.nonzero()[0].tolist()}: " \
         f"{got[bad][0].item()} vs {ref[bad][0].item()}"
+
+
+def dw_bound(tokens, hidden):
+    """d_weight's additions and its terms' error, in u of the sum of magnitudes."""
+    chunks = min(tokens, 2368 if hidden <= 1024 else 592 if hidden <= 4096 else 296)
+    return (-(-tokens // chunks) + -(-chunks // 32) + 36 + 32) * U
 
 
 def ref_y(h, w):
@@ -80,14 +88,14 @@ def test_forward_and_backward(dtype, hidden, tokens, cuda_device):
         dx, dw = pkg.situ_glu_rms_norm_bwd(dev[3], h, dev[1], EPS, grad_h=g)
         rdx, scale, rdw, mag = ref_grads(hs, w, gy, gh if g is not None else None)
         close(dx, rdx, half * rdx.abs() + 64 * U * scale + tiny, "d_x")
-        close(dw, rdw, HALF[wdtype] * rdw.abs() + (-(-tokens // 296) + 80) * U * mag + tiny, "d_weight")
+        close(dw, rdw, HALF[wdtype] * rdw.abs() + dw_bound(tokens, hidden) * mag + tiny, "d_weight")
     dx2, none = pkg.situ_glu_rms_norm_bwd(dev[3], h, dev[1], EPS, want_dw=False)
     assert none is None and torch.equal(dx2, dx)
 
 
 @pytest.mark.parametrize("rule", ["ocp", "ceil"])
 @pytest.mark.parametrize("dtype,hidden", [(torch.bfloat16, 32), (torch.bfloat16, 992), (torch.bfloat16, 4128),
-                                          (torch.float32, 64), (torch.float32, 2080)])
+                                          (torch.bfloat16, 8192), (torch.float32, 64), (torch.float32, 2080)])
 def test_mxfp8(dtype, hidden, rule, cuda_device):
     tokens = 19
     x, r = make(dtype, tokens, hidden, 11), make(dtype, tokens, hidden, 12, 3.0)
@@ -103,9 +111,9 @@ def test_mxfp8(dtype, hidden, rule, cuda_device):
     assert torch.equal(h, h2)
 
 
-def test_many_rows_and_the_launch_size(cuda_device):
+@pytest.mark.parametrize("tokens,hidden", [(1500, 520), (5001, 256), (1300, 1544), (700, 7176)])
+def test_many_rows_and_the_launch_size(tokens, hidden, cuda_device):
     """More rows than chunks and CTAs; every result is the same under any launch cap."""
-    tokens, hidden = 1500, 520
     args = [make(torch.bfloat16, tokens, hidden, s).to(cuda_device) for s in (21, 22, 23, 24)]
     w = torch.linspace(0.5, 1.5, hidden, device=cuda_device)
     h, gy, gh = args[0], args[1], args[2]
@@ -117,7 +125,7 @@ def test_many_rows_and_the_launch_size(cuda_device):
     first = everything()
     rdx, scale, rdw, mag = ref_grads(h.cpu(), w.cpu(), gy.cpu(), gh.cpu())
     close(first[2], rdx, HALF[torch.bfloat16] * rdx.abs() + 64 * U * scale, "d_x")
-    close(first[3], rdw, U * rdw.abs() + (6 + 80) * U * mag, "d_weight")
+    close(first[3], rdw, U * rdw.abs() + dw_bound(tokens, hidden) * mag, "d_weight")
     for cap in (1, 7):
         prev = abi.situ_glu_set_max_ctas(cap)
         try:
