@@ -384,18 +384,42 @@ __global__ void __launch_bounds__(kStoreThreads) situ_nvfp4_dequantize_kernel(co
 // cores multiply the codes by their block scales and add in fp32; the two
 // tensor scales, one number per expert, are applied once in the epilogue.
 //
-// Structure (one CTA per SM, persistent over output tiles of 128 rows and BN
-// columns, numbered expert by expert as in situ_fused_gemm.cuh):
-//   * warp 0 streams the codes with TMA: a stage is 256 elements of k, i.e. a
+// A cluster of two CTAs (tcgen05 cta_group::2), persistent over the output tiles of
+// 256 rows and BN = 256 or 128 columns, numbered expert by expert as in
+// situ_fused_gemm.cuh.  One product is M = 256, N = BN, k = 64: CTA r stages rows
+// [128 r, 128 r + 128) of the A tile and its half of the B tile and holds
+// accumulator rows [128 r, ...) in its TMEM.
+//   * warp 0 streams the codes with TMA, a stage being 256 elements of k, i.e. a
 //     128-byte swizzle row of A and of B;
-//   * warps 6 .. bring the block scales.  The tensor cores read them from TMEM in
-//     32-lane x 4-column atoms (512 bytes for 128 rows and 64 elements of k:
-//     row r's four scales at lane r % 32, column r / 32), while memory has them
-//     row by row, 16 bytes for a stage's 256 elements (scale_rows below);
-//   * warp 1 copies each stage's atoms to TMEM (tcgen05.cp, in issue order with
-//     the products that read them) and issues four products (k = 64 each);
-//   * two accumulators let warps 2-5 store one tile while the next one runs.
+//   * warps 6-9 write the block scales to TMEM, where the tensor cores read them
+//     (32-lane x 4-column atoms: row r's four scales of a product at lane r % 32,
+//     column r / 32), the same to each quarter of the lanes;
+//   * warp 1 of CTA 0 issues four products a stage;
+//   * warps 2-5 store the accumulator, one row a thread.
 // Every wait is bounded as in situ_fused_gemm.cuh.
+//
+// Two SMs a tile: per operation of the tensor cores an SM then moves 5 / 8 of the
+// operand bytes of one-SM tiles of 128 x 192, which spent 640 cycles a stage on
+// them for 384 of products (8192 x 7168 x 4096: 177 us, this form 94 us; 8 x 7168 x
+// 2048: 22, 16).  Scales by tcgen05.st: the tensor pipe takes about 55 cycles for
+// each 512-byte tcgen05.cp and runs no product meanwhile (154 us that way).
+//
+// The scales of four stages come in one go, 64 bytes of each row (64-byte swizzle);
+// lane l of each scale warp takes rows l, l + 32, ... of a stage and has in its
+// registers just the TMEM columns of its lane.  Where every row of scales starts on
+// 16 bytes they are a TMA box, issued in line with the codes; otherwise (rows of k /
+// 16 bytes, k not a multiple of 256) warps 10 and 11 copy them, eight or four bytes
+// at a time (8192 x 7168 x 4096: 97 and 119 us, by TMA 94 us; copied by the scale
+// warps themselves, between their writes to TMEM, 114 and 132 us).
+//
+// The epilogue drains the accumulator to registers before it stores (bf16), so
+// the next tile's products wait for the drain alone, and turns rows into whole
+// 128-byte lines through shared memory (16384 x 1024 x 4096 with a 16-byte piece
+// of 32 rows per store: 33 of 87 us).
+//
+// Waits poll with CTA scope; where the other CTA's work is waited for, one
+// acquire at cluster scope follows.  (Polling with cluster scope empties L1 each
+// time: 8192 x 7168 x 4096 took 253 us.)
 
 namespace nvgemm {
 
@@ -406,39 +430,42 @@ using fc1::tc_fence_after;
 using fc1::tc_fence_before;
 using fc1::Tile;
 using fc1::tma_load_2d;
+using fc1::tma_load_2d_pair;
 using fc1::tmem_ld16;
 using fc1::tmem_ld_wait;
-using fc1::umma_commit;
+using fc1::umma_commit_pair;
+using fc1::umma_commit_pair_local;
 using fc1::wait_or_abort;
 
-constexpr int kBM = 128;
+constexpr int kBM = 256;               // rows of a tile, 128 of them a CTA's
 constexpr int kStageK = 256;           // elements of k per stage
 constexpr int kStageRow = 128;         // their bytes
 constexpr int kSteps = 4;              // products (k = 64) per stage
-constexpr int kAtom = 512;             // bytes of scales of 128 rows and one step
 constexpr int kMaxExperts = 1024;
 constexpr int kHeader = 256;
+constexpr int kEpiWarps = 4;
+constexpr int kScaleWarps = 4;         // one per quarter of the TMEM lanes
+constexpr int kCopyWarps = 2;
+constexpr int kThreads = 32 * (2 + kEpiWarps + kScaleWarps + kCopyWarps);
+constexpr int kOutBytes = 32 * 128;    // a warp's piece of the output
 
 // Sizes of a kernel with BN output columns per tile.
 template <int BN>
 struct Shape {
-  static constexpr int kScaleAtoms = (BN + 127) / 128;  // of B, per step
-  static constexpr int kScaleWarps = 1 + kScaleAtoms;
-  static constexpr int kThreads = 192 + 32 * kScaleWarps;
-  static constexpr int kABytes = kBM * kStageRow;
-  static constexpr int kBBytes = BN * kStageRow;
-  static constexpr int kScaleBytes = kSteps * kAtom * (1 + kScaleAtoms);
-  static constexpr int kStageBytes = kABytes + kBBytes + kScaleBytes;
-  static constexpr int kStages = (220 * 1024) / kStageBytes < 8 ? (220 * 1024) / kStageBytes : 8;
-  static constexpr int kScaleCols = kSteps * 4 * (1 + kScaleAtoms);  // TMEM columns of a stage's scales
-  // TMEM: two accumulators, then the scales of two stages
-  static constexpr int kScaleBase = 2 * BN;
-  static constexpr int kTmemCols = kScaleBase + 2 * kScaleCols <= 256 ? 256 : 512;
-  static_assert(kScaleBase + 2 * kScaleCols <= 512, "TMEM overflows");
-  static_assert(kBBytes % 1024 == 0 && kScaleBytes % 1024 == 0, "stages keep the 1024-byte alignment");
+  static constexpr int kABytes = 128 * kStageRow, kBBytes = BN / 2 * kStageRow;
+  static constexpr int kStageBytes = kABytes + kBBytes;
+  static constexpr int kStages = BN == 256 ? 4 : 6;
+  static constexpr int kAccs = 256 / BN;                      // accumulators
+  static constexpr int kScaleRows = 128 + BN;                 // scales of a stage: A's rows, then B's
+  static constexpr int kGroupBytes = kScaleRows * 64;         // of four stages
+  static constexpr int kGroups = BN / 32;                     // TMEM columns of B's scales per step
+  static constexpr int kScaleCols = kSteps * (4 + kGroups);   // of a stage
+  static constexpr int kScaleBase = kAccs * BN;
+  static constexpr int kSmem = kStages * kStageBytes + 2 * kGroupBytes + kEpiWarps * kOutBytes;
+  static_assert(kScaleBase + kStages * kScaleCols <= 512, "TMEM overflows");
   // kind::mxf4nvf4: E2M1 A and B (bits 7-9, 10-11 = 1), K-major, N >> 3 at bits
   // 17-22, UE4M3 scales (bit 23 = 0), M >> 7 at bits 27-28, scale ids 0, k = 64.
-  static constexpr uint32_t kIdesc = (1u << 7) | (1u << 10) | (static_cast<uint32_t>(BN >> 3) << 17) | (1u << 27);
+  static constexpr uint32_t kIdesc = (1u << 7) | (1u << 10) | (static_cast<uint32_t>(BN >> 3) << 17) | (2u << 27);
 };
 
 struct Args {
@@ -453,360 +480,11 @@ struct Args {
   int experts;
   int64_t tokens;
   int k, n;
-  int a_vec, w_vec;  // the scales of a stage load as one 16-byte vector
+  int scale_bytes;  // 16: the scales come by TMA; 8, 4: by copies of so many bytes
   char* out;
   int64_t out_pitch;
   int out_bf16;
 };
-
-// Descriptor of a 512-byte scale atom for tcgen05.cp.32x128b: no swizzle, rows
-// of 16 bytes, groups of 8 rows 128 bytes apart, descriptor version 1.
-__device__ __forceinline__ uint64_t atom_desc(uint32_t addr) {
-  return static_cast<uint64_t>((addr >> 4) & 0x3fffu) | (static_cast<uint64_t>(128 >> 4) << 32) |
-         (static_cast<uint64_t>(1) << 46);
-}
-// The whole warp comes here and one lane (`lead`) issues, so that the operands
-// stay in uniform registers; the same for the product below.
-__device__ __forceinline__ void scale_cp(uint32_t tmem, uint64_t desc, uint32_t lead) {
-  asm volatile(
-      "{\n\t.reg .pred q;\n\t"
-      "setp.ne.b32 q, %2, 0;\n\t"
-      "@q tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n\t}" ::"r"(tmem),
-      "l"(desc), "r"(lead)
-      : "memory");
-}
-__device__ __forceinline__ void umma_nvfp4(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t sfa,
-                                           uint32_t sfb, uint32_t accumulate, uint32_t lead) {
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.b32 p, %6, 0;\n\t"
-      "setp.ne.b32 q, %7, 0;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate), "r"(lead)
-      : "memory");
-}
-
-// The 16 scales of one row and stage: `words` groups of four (64 elements of
-// k) exist, the others are zero.
-__device__ __forceinline__ uint4 load_scales(const uint8_t* p, int words, int vec) {
-  if (vec && words >= 4) return __ldg(reinterpret_cast<const uint4*>(p));
-  const uint32_t* q = reinterpret_cast<const uint32_t*>(p);
-  uint4 r = make_uint4(0, 0, 0, 0);
-  if (words > 0) r.x = __ldg(q);
-  if (words > 1) r.y = __ldg(q + 1);
-  if (words > 2) r.z = __ldg(q + 2);
-  if (words > 3) r.w = __ldg(q + 3);
-  return r;
-}
-
-// One warp's share of a tile's block scales: 128 rows (the first `left` exist)
-// of every stage.  Four stages come in one go: lane (rr, j) = (lane / 4, lane %
-// 4) loads stage j's 16 scales of rows rr, rr + 8, ..., so that four lanes read
-// 64 bytes of a row (a load that took 16 bytes from each of 32 rows cost as much
-// of the L1 and shared-memory path as the products' operands).  The lane then
-// has rows l, l + 32, l + 64, l + 96 for each of its l = 8 q + rr: the words of a
-// step's atom that belong together, stored as one vector when its stage's turn
-// comes.  take(stage) waits for a free stage and gives the address of its first
-// atom (the next step's is `apart` bytes on) or NULL to stop; put(stage) hands
-// the stage over.
-template <class Take, class Put>
-__device__ __forceinline__ bool scale_rows(const uint8_t* rows, int64_t pitch, int64_t left, int k, int k_blocks, int vec,
-                                           int apart, Take take, Put put) {
-  const int lane = threadIdx.x & 31, rr = lane >> 2, j = lane & 3;
-  const uint8_t* p = rows + rr * pitch + j * 16;
-  for (int kg = 0; kg < k_blocks; kg += 4, p += 64) {
-    const int words = (k - (kg + j) * kStageK) / 64;  // <= 0 past the end
-    uint4 v[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-      v[i] = 8 * i + rr < left ? load_scales(p + i * 8 * pitch, words, vec) : make_uint4(0, 0, 0, 0);
-    for (int u = 0; u < 4 && kg + u < k_blocks; ++u) {
-      unsigned char* st = take();
-      if (st == nullptr) return false;
-      if (j == u) {
-        st += rr * 16;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          *reinterpret_cast<uint4*>(st + q * 128) = make_uint4(v[q].x, v[q + 4].x, v[q + 8].x, v[q + 12].x);
-          *reinterpret_cast<uint4*>(st + q * 128 + apart) = make_uint4(v[q].y, v[q + 4].y, v[q + 8].y, v[q + 12].y);
-          *reinterpret_cast<uint4*>(st + q * 128 + 2 * apart) = make_uint4(v[q].z, v[q + 4].z, v[q + 8].z, v[q + 12].z);
-          *reinterpret_cast<uint4*>(st + q * 128 + 3 * apart) = make_uint4(v[q].w, v[q + 4].w, v[q + 8].w, v[q + 12].w);
-        }
-      }
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the copies to TMEM read them
-      __syncwarp();
-      put();
-    }
-  }
-  return true;
-}
-
-template <int BN>
-__global__ void __launch_bounds__(Shape<BN>::kThreads, 1)
-    situ_nvfp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_w,
-                           const Args a) {
-  using P = Shape<BN>;
-  extern __shared__ unsigned char smem_raw[];
-  const uint32_t raw_addr = smem_u32(smem_raw);
-  unsigned char* ring = smem_raw + ((1024u - (raw_addr & 1023u)) & 1023u);
-  unsigned char* header = ring + P::kStages * P::kStageBytes;
-  uint64_t* full = reinterpret_cast<uint64_t*>(header);
-  uint64_t* empty = full + P::kStages;
-  uint64_t* acc_full = empty + P::kStages;
-  uint64_t* acc_empty = acc_full + 2;
-  uint64_t* drain = acc_empty + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  static_assert((2 * P::kStages + 5) * 8 + 8 <= kHeader, "header overflows");
-  int64_t* lo = reinterpret_cast<int64_t*>(header + kHeader);
-  int64_t* hi = lo + a.experts;
-  int* first_tile = reinterpret_cast<int*>(hi + a.experts);
-
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int n_tiles = (a.n + BN - 1) / BN;
-  const int k_blocks = (a.k + kStageK - 1) / kStageK;
-
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < P::kStages; ++s) {
-      mbar_init(&full[s], 1 + P::kScaleWarps);  // the TMA warp and each scale warp
-      mbar_init(&empty[s], 1);                  // the MMA warp's commit
-    }
-    for (int b = 0; b < 2; ++b) {
-      mbar_init(&acc_full[b], 1);
-      mbar_init(&acc_empty[b], 128);
-    }
-    mbar_init(drain, 1);
-    *abort_flag = 0;
-    mbar_fence_init();
-  }
-  if (warp == 0) scan_experts<kBM>(a, n_tiles, lane, lo, hi, first_tile);
-  if (warp == 1) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
-                 "r"(P::kTmemCols)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem_base = *tmem_slot;
-  const int total = first_tile[a.experts];
-
-  if (warp == 0) {
-    // ---- codes ----
-    int stage = 0;
-    uint32_t phase = 0, issued = 0;
-    bool ok = true;
-    for (int t = blockIdx.x; ok && t < total; t += gridDim.x) {
-      const Tile tile = decode_tile<kBM>(t, first_tile, lo, hi, a.experts, n_tiles, BN);
-      const int32_t wrow = tile.expert * a.n + tile.n0;
-      for (int kb = 0; kb < k_blocks; ++kb) {
-        if (!wait_or_abort(&empty[stage], phase ^ 1u, abort_flag)) {
-          ok = false;
-          break;
-        }
-        if (lane == 0) {
-          unsigned char* st = ring + stage * P::kStageBytes;
-          mbar_arrive_expect_tx(&full[stage], P::kABytes + P::kBBytes);
-          tma_load_2d(st, &tmap_a, kb * kStageRow, static_cast<int32_t>(tile.m0), &full[stage]);
-          tma_load_2d(st + P::kABytes, &tmap_w, kb * kStageRow, wrow, &full[stage]);
-        }
-        __syncwarp();
-        issued |= 1u << stage;
-        if (++stage == P::kStages) {
-          stage = 0;
-          phase ^= 1u;
-        }
-      }
-    }
-    if (!ok) {
-      // Aborted: let the copies this warp issued land (bounded) before the CTA exits.
-      for (int s = 0; s < P::kStages; ++s) {
-        if (!(issued & (1u << s))) continue;
-        const uint32_t ph = (s < stage) ? phase : (phase ^ 1u);
-        const unsigned long long t0 = global_timer_ns();
-        while (!mbar_try_wait(&full[s], ph) && global_timer_ns() - t0 < kWaitLimitNs) {
-        }
-      }
-    }
-  } else if (warp == 1) {
-    // ---- products ----
-    int stage = 0, it = 0, buf = 0;
-    uint32_t phase = 0, acc_phase = 0;
-    bool ok = true;
-    for (int t = blockIdx.x; ok && t < total; t += gridDim.x, ++it) {
-      const int b = it & 1;
-      if (!wait_or_abort(&acc_empty[b], ((acc_phase >> b) & 1u) ^ 1u, abort_flag)) break;
-      tc_fence_after();
-      const uint32_t d = tmem_base + static_cast<uint32_t>(b * BN);
-      for (int kb = 0; kb < k_blocks; ++kb) {
-        if (!wait_or_abort(&full[stage], phase, abort_flag)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const uint32_t a_addr = smem_u32(ring + stage * P::kStageBytes);
-        const uint64_t adesc = smem_desc_sw128(a_addr), bdesc = smem_desc_sw128(a_addr + P::kABytes);
-        const uint64_t sc = atom_desc(a_addr + P::kABytes + P::kBBytes);
-        const uint32_t sfa = tmem_base + P::kScaleBase + static_cast<uint32_t>(buf * P::kScaleCols);
-        const uint32_t sfb = sfa + kSteps * 4;
-#pragma unroll
-        for (int i = 0; i < kSteps * (1 + P::kScaleAtoms); ++i) scale_cp(sfa + 4 * i, sc + i * (kAtom / 16), lane == 0);
-#pragma unroll
-        for (int s = 0; s < kSteps; ++s)
-          umma_nvfp4(d, adesc + 2 * s, bdesc + 2 * s, P::kIdesc, sfa + 4 * s, sfb + 4 * P::kScaleAtoms * s,
-                     (kb | s) != 0 ? 1u : 0u, lane == 0);
-        if (lane == 0) umma_commit(&empty[stage]);
-        __syncwarp();
-        buf ^= 1;
-        if (++stage == P::kStages) {
-          stage = 0;
-          phase ^= 1u;
-        }
-      }
-      if (!ok) break;
-      if (lane == 0) umma_commit(&acc_full[b]);
-      __syncwarp();
-      acc_phase ^= 1u << b;
-    }
-    if (!ok || *abort_flag) {
-      if (lane == 0) umma_commit(drain);
-      __syncwarp();
-      const unsigned long long t0 = global_timer_ns();
-      while (!mbar_try_wait(drain, 0) && global_timer_ns() - t0 < kWaitLimitNs) {
-      }
-    }
-  } else if (warp < 6) {
-    // ---- epilogue: one accumulator row per thread ----
-    const int quarter = warp & 3;
-    const double unit_a = static_cast<double>(*a.a_amax) / 2688.0;
-    uint32_t acc_phase = 0;
-    int it = 0;
-    for (int t = blockIdx.x; t < total; t += gridDim.x, ++it) {
-      const int b = it & 1;
-      if (!wait_or_abort(&acc_full[b], (acc_phase >> b) & 1u, abort_flag)) break;
-      tc_fence_after();
-      const Tile tile = decode_tile<kBM>(t, first_tile, lo, hi, a.experts, n_tiles, BN);
-      const float alpha =
-          static_cast<float>(unit_a * (static_cast<double>(a.w_amax[tile.expert * a.w_amax_stride]) / 2688.0));
-      const int64_t row = tile.m0 + quarter * 32 + lane;
-      const bool valid = row < tile.m_end;
-      const int cols = min(BN, a.n - tile.n0);
-      const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(b * BN);
-      char* out = a.out + (valid ? row : 0) * a.out_pitch + static_cast<int64_t>(tile.n0) * (a.out_bf16 ? 2 : 4);
-#pragma unroll 1
-      for (int c = 0; c < cols; c += 16) {  // uniform over the warp
-        uint32_t r[16];
-        tmem_ld16(taddr + c, r);
-        tmem_ld_wait(r);
-        float v[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]) * alpha;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (!valid || c + 8 * h >= cols) continue;
-          const float* w = v + 8 * h;
-          if (a.out_bf16) {
-            *reinterpret_cast<uint4*>(out + (c + 8 * h) * 2) =
-                make_uint4(Bf16::pack(make_float2(w[0], w[1])), Bf16::pack(make_float2(w[2], w[3])),
-                           Bf16::pack(make_float2(w[4], w[5])), Bf16::pack(make_float2(w[6], w[7])));
-          } else {
-            float4* o = reinterpret_cast<float4*>(out + (c + 8 * h) * 4);
-            o[0] = make_float4(w[0], w[1], w[2], w[3]);
-            o[1] = make_float4(w[4], w[5], w[6], w[7]);
-          }
-        }
-        __syncwarp();
-      }
-      tc_fence_before();
-      mbar_arrive(&acc_empty[b]);
-      acc_phase ^= 1u << b;
-    }
-  } else {
-    // ---- block scales: warp 6 the rows of A, warp 7 + j rows [128 j, 128 j + 128) of B ----
-    const int part = warp - 6;
-    const bool is_a = part == 0;
-    const uint8_t* base = is_a ? a.a_scale : a.w_scale;
-    const int64_t pitch = is_a ? a.a_scale_pitch : a.w_scale_pitch;
-    const int vec = is_a ? a.a_vec : a.w_vec;
-    int stage = 0;
-    uint32_t phase = 0;
-    bool ok = true;
-    auto take = [&]() -> unsigned char* {
-      if (!wait_or_abort(&empty[stage], phase ^ 1u, abort_flag)) return nullptr;
-      return ring + stage * P::kStageBytes + P::kABytes + P::kBBytes + (is_a ? 0 : kSteps * kAtom + (part - 1) * kAtom);
-    };
-    auto put = [&]() {
-      if (lane == 0) mbar_arrive(&full[stage]);
-      if (++stage == P::kStages) {
-        stage = 0;
-        phase ^= 1u;
-      }
-    };
-    for (int t = blockIdx.x; ok && t < total; t += gridDim.x) {
-      const Tile tile = decode_tile<kBM>(t, first_tile, lo, hi, a.experts, n_tiles, BN);
-      // first row of this warp's 128 and how many of them exist
-      const int64_t row0 = is_a ? tile.m0 : static_cast<int64_t>(tile.expert) * a.n + tile.n0 + (part - 1) * 128;
-      const int64_t left = is_a ? tile.m_end - tile.m0 : min(a.n - tile.n0, BN) - (part - 1) * 128;
-      ok = scale_rows(base + row0 * pitch, pitch, left, a.k, k_blocks, vec, (is_a ? 1 : P::kScaleAtoms) * kAtom, take,
-                      put);
-    }
-  }
-
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  if (warp == 1)
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(P::kTmemCols) : "memory");
-}
-
-// ---- Two-SM form (tcgen05 cta_group::2) ---------------------------------------
-// A cluster of two CTAs computes a 256 x 256 tile (one product: M = 256, N =
-// 256, k = 64): CTA r stages rows [128 r, 128 r + 128) of the A tile and of the
-// B tile and holds accumulator rows [128 r, ...) in its TMEM.  Per operation of
-// the tensor cores an SM moves 5 / 8 of the one-SM form's operand bytes, and the
-// one-SM form is bound by just these: at 192 columns a stage's 40 KB are written
-// to and read from shared memory in 640 cycles, the products take 384.
-//
-// Each CTA needs its own rows' scales and every column's.  Four warps write them
-// to TMEM themselves (tcgen05.st, each its 32 lanes): the tensor pipe takes about
-// 55 cycles for each 512-byte tcgen05.cp and runs no product meanwhile, 660
-// cycles a stage next to 512 of products (8192 x 7168 x 4096: 154 us that way).
-// The scales of four stages are one TMA box (64 bytes of each row, 64-byte
-// swizzle), issued in line with the codes: loads by the warps themselves waited
-// behind the ring's copies in the memory queue, longer than a register prefetch
-// of four stages covers (141 us for 104).  Lane l of each warp then takes rows l,
-// l + 32, ... and has in its registers just the TMEM columns of its lane.  TMEM
-// holds one accumulator (256 columns) and every ring stage's scales (4 x 48).
-//
-// The epilogue drains the accumulator to registers before it stores (bf16), so
-// the next tile's products wait for the drain alone, and turns rows into whole
-// 128-byte lines through shared memory (16384 x 1024 x 4096 with a 16-byte piece
-// of 32 rows per store: 33 of 87 us).
-//
-// Waits poll with CTA scope; where the other CTA's work is waited for, one
-// acquire at cluster scope follows.  (Polling with cluster scope empties L1 each
-// time and held up the scales' loads: 8192 x 7168 x 4096 took 253 us.)
-
-constexpr int kBN2 = 256, kBM2 = 256;
-constexpr int kPairEpiWarps = 4;
-constexpr int kPairScaleWarps = 4;  // one per quarter of the TMEM lanes
-constexpr int kPairThreads = 32 * (2 + kPairEpiWarps + kPairScaleWarps);
-constexpr int kPairABytes = 128 * kStageRow, kPairBBytes = 128 * kStageRow;
-constexpr int kPairStageBytes = kPairABytes + kPairBBytes;
-constexpr int kPairStages = 4;
-constexpr int kPairScaleRows = 128 + kBN2;               // scales of a stage: A's rows, then B's
-constexpr int kPairGroupBytes = kPairScaleRows * 64;     // of four stages
-constexpr int kPairScaleCols = kPairScaleRows / 32 * 4;  // TMEM columns of a stage's scales
-constexpr int kPairScaleBase = kBN2;
-constexpr int kPairOutBytes = 32 * 128;                  // a warp's piece of the output
-constexpr int kPairSmem = kPairStages * kPairStageBytes + 2 * kPairGroupBytes + kPairEpiWarps * kPairOutBytes;
-static_assert(kPairScaleBase + kPairStages * kPairScaleCols <= 512, "two-SM TMEM overflows");
-constexpr uint32_t kPairIdesc = (1u << 7) | (1u << 10) | (static_cast<uint32_t>(kBN2 >> 3) << 17) | (2u << 27);
-
-using fc1::tma_load_2d_pair;
-using fc1::umma_commit_pair;
-using fc1::umma_commit_pair_local;
 
 __device__ __forceinline__ bool wait_or_abort_acquire(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
   if (!wait_or_abort(bar, parity, abort_flag)) return false;
@@ -816,14 +494,14 @@ __device__ __forceinline__ bool wait_or_abort_acquire(uint64_t* bar, uint32_t pa
 
 // The whole warp comes here and one lane (`lead`) issues, so that the operands
 // stay in uniform registers.
-__device__ __forceinline__ void umma_nvfp4_pair(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t sfa, uint32_t sfb,
-                                                uint32_t accumulate, uint32_t lead) {
+__device__ __forceinline__ void umma_nvfp4_pair(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t sfa,
+                                                uint32_t sfb, uint32_t accumulate, uint32_t lead) {
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.b32 p, %6, 0;\n\t"
       "setp.ne.b32 q, %7, 0;\n\t"
       "@q tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
-      "l"(adesc), "l"(bdesc), "r"(kPairIdesc), "r"(sfa), "r"(sfb), "r"(accumulate), "r"(lead)
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate), "r"(lead)
       : "memory");
 }
 // Arrive on an mbarrier of either CTA after TMEM writes that are complete
@@ -868,52 +546,81 @@ __device__ __forceinline__ void put_piece(unsigned char* piece, const Args& a, c
 }
 __device__ __forceinline__ uint32_t word(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
 
-__global__ void __launch_bounds__(kPairThreads, 1)
-    situ_nvfp4_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_w,
+// Copies G bytes to shared memory of which `real` (0 to G) are read, the rest zero.
+template <int G>
+__device__ __forceinline__ void cp_async(unsigned char* dst, const uint8_t* src, int real) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(smem_u32(dst)), "l"(src), "n"(G), "r"(real) : "memory");
+}
+// The copy warps' part of a group of scales: 64 bytes (four stages, from byte k0 of
+// the row on) of `rows` rows, of which the first `left` exist and have `width` bytes;
+// as the TMA box has them (16-byte chunks swizzled by (row / 2) % 4, zeros outside).
+template <int G>
+__device__ __forceinline__ void copy_scales(unsigned char* dst, const uint8_t* base, int64_t pitch, int64_t left, int rows,
+                                            int k0, int width) {
+  constexpr int kPer = 64 / G, kPass = 32 * kCopyWarps / kPer;  // pieces of a row, rows of a pass
+  const int x = static_cast<int>(threadIdx.x) - (kThreads - 32 * kCopyWarps);
+  const int off = x % kPer * G;
+  const int in = max(0, min(G, width - k0 - off));
+  const uint8_t* src = base + (x / kPer) * pitch + k0 + off;
+#pragma unroll 4
+  for (int r = x / kPer; r < rows; r += kPass, src += kPass * pitch) {
+    const int real = r < left ? in : 0;
+    cp_async<G>(dst + r * 64 + (((off >> 4) ^ ((r >> 1) & 3)) << 4) + (off & 15), real != 0 ? src : base, real);
+  }
+}
+
+template <int BN>
+__global__ void __launch_bounds__(kThreads, 1)
+    situ_nvfp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_w,
                                 const __grid_constant__ CUtensorMap tmap_as, const __grid_constant__ CUtensorMap tmap_ws,
                                 const Args a) {
+  using P = Shape<BN>;
   extern __shared__ unsigned char smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
   unsigned char* ring = smem_raw + ((1024u - (raw_addr & 1023u)) & 1023u);
-  unsigned char* scales = ring + kPairStages * kPairStageBytes;
-  unsigned char* pieces = scales + 2 * kPairGroupBytes;
-  unsigned char* header = ring + kPairSmem;
+  unsigned char* scales = ring + P::kStages * P::kStageBytes;
+  unsigned char* pieces = scales + 2 * P::kGroupBytes;
+  unsigned char* header = ring + P::kSmem;
   uint64_t* full = reinterpret_cast<uint64_t*>(header);
-  uint64_t* empty = full + kPairStages;
-  uint64_t* acc_full = empty + kPairStages;
-  uint64_t* acc_empty = acc_full + 1;
-  uint64_t* sf_full = acc_empty + 1;  // [2]: this CTA's scales of four stages
+  uint64_t* empty = full + P::kStages;
+  uint64_t* acc_full = empty + P::kStages;
+  uint64_t* acc_empty = acc_full + P::kAccs;
+  uint64_t* sf_full = acc_empty + P::kAccs;  // [2]: this CTA's scales of four stages
   uint64_t* sf_empty = sf_full + 2;
   uint64_t* drain = sf_empty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  static_assert((2 * P::kStages + 2 * P::kAccs + 5) * 8 + 8 <= kHeader, "header overflows");
   int64_t* lo = reinterpret_cast<int64_t*>(header + kHeader);
   int64_t* hi = lo + a.experts;
   int* first_tile = reinterpret_cast<int*>(hi + a.experts);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const bool own_scales = a.scale_bytes < 16;  // the copy warps bring them
   const uint32_t rank = cluster_rank();
   const bool leader = rank == 0;
   const int cl = static_cast<int>(cluster_index()), ncl = static_cast<int>(cluster_count());
-  const int n_tiles = (a.n + kBN2 - 1) / kBN2;
+  const int n_tiles = (a.n + BN - 1) / BN;
   const int k_blocks = (a.k + kStageK - 1) / kStageK;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kPairStages; ++s) {
-      mbar_init(&full[s], 1 + 2 * kPairScaleWarps);  // CTA 0's: its TMA warp, both CTAs' scale warps and bytes
+    for (int s = 0; s < P::kStages; ++s) {
+      mbar_init(&full[s], 1 + 2 * kScaleWarps);  // CTA 0's: its TMA warp, both CTAs' scale warps and bytes
       mbar_init(&empty[s], 1);                       // CTA 0's commit, to both
     }
     for (int b = 0; b < 2; ++b) {
-      mbar_init(&sf_full[b], 1);
-      mbar_init(&sf_empty[b], kPairScaleWarps);
+      mbar_init(&sf_full[b], own_scales ? 32 * kCopyWarps : 1);
+      mbar_init(&sf_empty[b], kScaleWarps);
     }
-    mbar_init(acc_full, 1);
-    mbar_init(acc_empty, 2 * 32 * kPairEpiWarps);
+    for (int b = 0; b < P::kAccs; ++b) {
+      mbar_init(&acc_full[b], 1);
+      mbar_init(&acc_empty[b], 2 * 32 * kEpiWarps);
+    }
     mbar_init(drain, 1);
     *abort_flag = 0;
     mbar_fence_init();
   }
-  if (warp == 0) scan_experts<kBM2>(a, n_tiles, lane, lo, hi, first_tile);
+  if (warp == 0) scan_experts<kBM>(a, n_tiles, lane, lo, hi, first_tile);
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(512)
                  : "memory");
@@ -932,19 +639,21 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     uint32_t phase = 0, issued = 0;
     bool ok = true;
     for (int t = cl; ok && t < total; t += ncl) {
-      const Tile tile = decode_tile<kBM2>(t, first_tile, lo, hi, a.experts, n_tiles, kBN2);
+      const Tile tile = decode_tile<kBM>(t, first_tile, lo, hi, a.experts, n_tiles, BN);
       const int32_t arow = static_cast<int32_t>(tile.m0 + 128 * rank);
-      const int32_t wrow = tile.expert * a.n + tile.n0 + static_cast<int32_t>(128 * rank);
+      const int32_t wrow = tile.expert * a.n + tile.n0 + static_cast<int32_t>(BN / 2 * rank);
+      // a CTA none of whose rows exist multiplies what its ring holds, stored nowhere
+      const bool second = tile.m_end - tile.m0 > 128;
       for (int kb = 0; kb < k_blocks; ++kb) {
-        if ((kb & 3) == 0) {  // the scales of stages kb .. kb + 3
+        if (!own_scales && (kb & 3) == 0) {  // the scales of stages kb .. kb + 3
           const int b = group & 1;
           if (!wait_or_abort(&sf_empty[b], ((group >> 1) & 1) ^ 1, abort_flag)) {
             ok = false;
             break;
           }
           if (lane == 0) {
-            unsigned char* sc = scales + b * kPairGroupBytes;
-            mbar_arrive_expect_tx(&sf_full[b], kPairGroupBytes);
+            unsigned char* sc = scales + b * P::kGroupBytes;
+            mbar_arrive_expect_tx(&sf_full[b], P::kGroupBytes);
             tma_load_2d(sc, &tmap_as, kb * 16, arow, &sf_full[b]);
             tma_load_2d(sc + 128 * 64, &tmap_ws, kb * 16, tile.expert * a.n + tile.n0, &sf_full[b]);
           }
@@ -956,15 +665,15 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           break;
         }
         if (lane == 0) {
-          unsigned char* st = ring + stage * kPairStageBytes;
+          unsigned char* st = ring + stage * P::kStageBytes;
           const uint32_t bar = peer_addr(&full[stage], 0);
-          if (leader) mbar_arrive_expect_tx(&full[stage], 2 * (kPairABytes + kPairBBytes));
-          tma_load_2d_pair(st, &tmap_a, kb * kStageRow, arow, bar);
-          tma_load_2d_pair(st + kPairABytes, &tmap_w, kb * kStageRow, wrow, bar);
+          if (leader) mbar_arrive_expect_tx(&full[stage], (second ? 2 : 1) * P::kABytes + 2 * P::kBBytes);
+          if (leader || second) tma_load_2d_pair(st, &tmap_a, kb * kStageRow, arow, bar);
+          tma_load_2d_pair(st + P::kABytes, &tmap_w, kb * kStageRow, wrow, bar);
         }
         __syncwarp();
         issued |= 1u << stage;
-        if (++stage == kPairStages) {
+        if (++stage == P::kStages) {
           stage = 0;
           phase ^= 1u;
         }
@@ -980,7 +689,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       }
     }
     if (!ok && leader) {
-      for (int s = 0; s < kPairStages; ++s) {
+      for (int s = 0; s < P::kStages; ++s) {
         if (!(issued & (1u << s))) continue;
         const uint32_t ph = (s < stage) ? phase : (phase ^ 1u);
         const unsigned long long t0 = global_timer_ns();
@@ -991,11 +700,12 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   } else if (warp == 1) {
     if (leader) {
       // ---- products (CTA 0) ----
-      int stage = 0;
+      int stage = 0, b = 0;
       uint32_t phase = 0, acc_phase = 0;
       bool ok = true;
       for (int t = cl; ok && t < total; t += ncl) {
-        if (!wait_or_abort_acquire(acc_empty, acc_phase ^ 1u, abort_flag)) {
+        const uint32_t d = tmem_base + static_cast<uint32_t>(b * BN);
+        if (!wait_or_abort_acquire(&acc_empty[b], acc_phase ^ 1u, abort_flag)) {
           ok = false;
           break;
         }
@@ -1006,25 +716,28 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             break;
           }
           tc_fence_after();
-          const uint32_t a_addr = smem_u32(ring + stage * kPairStageBytes);
-          const uint64_t adesc = smem_desc_sw128(a_addr), bdesc = smem_desc_sw128(a_addr + kPairABytes);
-          const uint32_t sfa = tmem_base + kPairScaleBase + static_cast<uint32_t>(stage * kPairScaleCols);
+          const uint32_t a_addr = smem_u32(ring + stage * P::kStageBytes);
+          const uint64_t adesc = smem_desc_sw128(a_addr), bdesc = smem_desc_sw128(a_addr + P::kABytes);
+          const uint32_t sfa = tmem_base + P::kScaleBase + static_cast<uint32_t>(stage * P::kScaleCols);
           const uint32_t sfb = sfa + kSteps * 4;
 #pragma unroll
           for (int s = 0; s < kSteps; ++s)
-            umma_nvfp4_pair(tmem_base, adesc + 2 * s, bdesc + 2 * s, sfa + 4 * s, sfb + 8 * s, (kb | s) != 0 ? 1u : 0u,
-                            lane == 0);
+            umma_nvfp4_pair(d, adesc + 2 * s, bdesc + 2 * s, P::kIdesc, sfa + 4 * s, sfb + P::kGroups * s,
+                            (kb | s) != 0 ? 1u : 0u, lane == 0);
           if (lane == 0) umma_commit_pair(&empty[stage]);
           __syncwarp();
-          if (++stage == kPairStages) {
+          if (++stage == P::kStages) {
             stage = 0;
             phase ^= 1u;
           }
         }
         if (!ok) break;
-        if (lane == 0) umma_commit_pair(acc_full);
+        if (lane == 0) umma_commit_pair(&acc_full[b]);
         __syncwarp();
-        acc_phase ^= 1u;
+        if (++b == P::kAccs) {
+          b = 0;
+          acc_phase ^= 1u;
+        }
       }
       if (!ok || *abort_flag) {
         if (lane == 0) umma_commit_pair_local(drain);
@@ -1034,37 +747,41 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         }
       }
     }
-  } else if (warp < 2 + kPairEpiWarps) {
+  } else if (warp < 2 + kEpiWarps) {
     // ---- epilogue: one accumulator row per thread ----
     const int quarter = warp & 3;
     const double unit_a = static_cast<double>(*a.a_amax) / 2688.0;
-    const uint32_t empty_addr = peer_addr(acc_empty, 0);
-    const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16);
-    unsigned char* piece = pieces + (warp - 2) * kPairOutBytes;
+    unsigned char* piece = pieces + (warp - 2) * kOutBytes;
     uint32_t acc_phase = 0;
+    int b = 0;
     for (int t = cl; t < total; t += ncl) {
-      const Tile tile = decode_tile<kBM2>(t, first_tile, lo, hi, a.experts, n_tiles, kBN2);
-      const float alpha =
+      const uint32_t empty_addr = peer_addr(&acc_empty[b], 0);
+      const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(b * BN);
+      const Tile tile = decode_tile<kBM>(t, first_tile, lo, hi, a.experts, n_tiles, BN);
+      const float unit =
           static_cast<float>(unit_a * (static_cast<double>(a.w_amax[tile.expert * a.w_amax_stride]) / 2688.0));
       const int64_t row0 = tile.m0 + 128 * rank + quarter * 32;
-      const int cols = min(kBN2, a.n - tile.n0);
-      if (!wait_or_abort(acc_full, acc_phase, abort_flag)) break;
+      const int cols = min(BN, a.n - tile.n0);
+      if (!wait_or_abort(&acc_full[b], acc_phase, abort_flag)) break;
       tc_fence_after();
-      if (a.out_bf16) {
-        uint32_t q[kBN2 / 2];
+      if (row0 >= tile.m_end) {  // none of the warp's rows exists
+        tc_fence_before();
+        mbar_arrive_remote_relaxed(empty_addr);
+      } else if (a.out_bf16) {
+        uint32_t q[BN / 2];
 #pragma unroll
-        for (int c = 0; c < kBN2; c += 16) {
+        for (int c = 0; c < BN; c += 16) {
           uint32_t r[16];
           tmem_ld16(taddr + c, r);
           tmem_ld_wait(r);
 #pragma unroll
           for (int i = 0; i < 8; ++i)
-            q[c / 2 + i] = Bf16::pack(make_float2(__uint_as_float(r[2 * i]) * alpha, __uint_as_float(r[2 * i + 1]) * alpha));
+            q[c / 2 + i] = Bf16::pack(make_float2(__uint_as_float(r[2 * i]) * unit, __uint_as_float(r[2 * i + 1]) * unit));
         }
         tc_fence_before();
         mbar_arrive_remote_relaxed(empty_addr);
 #pragma unroll
-        for (int c = 0; c < kBN2; c += 64) put_piece(piece, a, tile, row0, &q[c / 2], c, cols, 8);
+        for (int c = 0; c < BN; c += 64) put_piece(piece, a, tile, row0, &q[c / 2], c, cols, 8);
       } else {
 #pragma unroll 1
         for (int c = 0; c < cols; c += 32) {  // uniform over the warp
@@ -1074,20 +791,23 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           tmem_ld_wait(r0, r1);
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            q[i] = __float_as_uint(__uint_as_float(r0[i]) * alpha);
-            q[16 + i] = __float_as_uint(__uint_as_float(r1[i]) * alpha);
+            q[i] = __float_as_uint(__uint_as_float(r0[i]) * unit);
+            q[16 + i] = __float_as_uint(__uint_as_float(r1[i]) * unit);
           }
           put_piece(piece, a, tile, row0, q, c, cols, 4);
         }
         tc_fence_before();
         mbar_arrive_remote_relaxed(empty_addr);
       }
-      acc_phase ^= 1u;
+      if (++b == P::kAccs) {
+        b = 0;
+        acc_phase ^= 1u;
+      }
     }
-  } else {
+  } else if (warp < 2 + kEpiWarps + kScaleWarps) {
     // ---- block scales (both CTAs): this CTA's rows of A, every column's of B ----
     const int quarter = warp & 3;
-    const uint32_t lanes = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + kPairScaleBase;
+    const uint32_t lanes = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + P::kScaleBase;
     int stage = 0, group = 0;
     uint32_t phase = 0;
     bool ok = true;
@@ -1105,26 +825,28 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           }
           tc_fence_after();
           // stage u's 16 bytes of row l: chunk u of the row's 64, swizzled by (row / 2) % 4
-          const unsigned char* st = scales + b * kPairGroupBytes + lane * 64 + ((u ^ ((lane >> 1) & 3)) * 16);
-          const uint32_t col = lanes + static_cast<uint32_t>(stage * kPairScaleCols);
-          uint4 q[12];
+          const unsigned char* st = scales + b * P::kGroupBytes + lane * 64 + ((u ^ ((lane >> 1) & 3)) * 16);
+          const uint32_t col = lanes + static_cast<uint32_t>(stage * P::kScaleCols);
+          constexpr int kRowGroups = 4 + P::kGroups;
+          uint4 q[kRowGroups];
 #pragma unroll
-          for (int c = 0; c < 12; ++c) q[c] = lds16(st + c * 2048);
+          for (int c = 0; c < kRowGroups; ++c) q[c] = lds16(st + c * 2048);
           uint32_t r[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) r[i] = word(q[i & 3], i >> 2);  // A: step i / 4, row group i % 4
           tmem_st16(col, r);
 #pragma unroll
-          for (int h2 = 0; h2 < 2; ++h2) {
+          for (int h = 0; h < P::kGroups / 4; ++h) {  // B: steps and groups in order
 #pragma unroll
-            for (int i = 0; i < 16; ++i) r[i] = word(q[4 + (i & 7)], 2 * h2 + (i >> 3));  // B: step 2 h2 + i / 8, group i % 8
-            tmem_st16(col + 16 + 16 * h2, r);
+            for (int i = 0; i < 16; ++i)
+              r[i] = word(q[4 + (16 * h + i) % P::kGroups], (16 * h + i) / P::kGroups);
+            tmem_st16(col + 16 + 16 * h, r);
           }
           asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive_remote_relaxed(peer_addr(&full[stage], 0));
-          if (++stage == kPairStages) {
+          if (++stage == P::kStages) {
             stage = 0;
             phase ^= 1u;
           }
@@ -1133,6 +855,34 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         if (ok && lane == 0) mbar_arrive(&sf_empty[b]);  // the warp has read the group
       }
     }
+  } else if (own_scales) {
+    // ---- copies of the block scales whose rows TMA cannot read ----
+    int group = 0;
+    bool ok = true;
+    for (int t = cl; ok && t < total; t += ncl) {
+      const Tile tile = decode_tile<kBM>(t, first_tile, lo, hi, a.experts, n_tiles, BN);
+      const int64_t arow = tile.m0 + 128 * rank, wrow = static_cast<int64_t>(tile.expert) * a.n + tile.n0;
+      const int64_t aleft = tile.m_end - arow, wleft = a.n - tile.n0;
+      const uint8_t* as = a.a_scale + (aleft > 0 ? arow : 0) * a.a_scale_pitch;
+      const uint8_t* ws = a.w_scale + wrow * a.w_scale_pitch;
+      for (int kg = 0; kg < k_blocks; kg += 4, ++group) {
+        const int b = group & 1;
+        if (!wait_or_abort(&sf_empty[b], ((group >> 1) & 1) ^ 1, abort_flag)) {
+          ok = false;
+          break;
+        }
+        unsigned char* sc = scales + b * P::kGroupBytes;
+        if (a.scale_bytes == 8) {
+          copy_scales<8>(sc, as, a.a_scale_pitch, aleft, 128, kg * 16, a.k / 16);
+          copy_scales<8>(sc + 128 * 64, ws, a.w_scale_pitch, wleft, BN, kg * 16, a.k / 16);
+        } else {
+          copy_scales<4>(sc, as, a.a_scale_pitch, aleft, 128, kg * 16, a.k / 16);
+          copy_scales<4>(sc + 128 * 64, ws, a.w_scale_pitch, wleft, BN, kg * 16, a.k / 16);
+        }
+        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&sf_full[b])) : "memory");
+      }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");  // the CTA leaves with no copy in flight
   }
 
   tc_fence_before();
@@ -1163,35 +913,12 @@ situ_status_t byte_map(CUtensorMap* m, const void* base, int64_t inner, int64_t 
   return SITU_OK;
 }
 
-template <int BN>
-situ_status_t launch(const void* a_data, int64_t a_pitch, const void* w_data, int64_t w_pitch, const Args& a,
-                     cudaStream_t s) {
-  using P = Shape<BN>;
-  CUtensorMap ma, mw;
-  situ_status_t st = byte_map(&ma, a_data, a.k / 2, a.tokens, a_pitch, kStageRow, kBM);
-  if (st != SITU_OK) return st;
-  st = byte_map(&mw, w_data, a.k / 2, static_cast<int64_t>(a.experts) * a.n, w_pitch, kStageRow, BN);
-  if (st != SITU_OK) return st;
-  int grid = 0;
-  st = device_sm_count(&grid);
-  if (st != SITU_OK) return st;
-  const int cap = g_max_ctas.load(std::memory_order_relaxed);
-  if (cap > 0 && grid > cap) grid = cap;
-  // no more CTAs than tiles there can be: every expert may end in a part of one
-  const int64_t most = ((a.tokens + kBM - 1) / kBM + a.experts - 1) * ((a.n + BN - 1) / BN);
-  if (grid > most) grid = static_cast<int>(most);
-  const int smem = 1024 + P::kStages * P::kStageBytes + kHeader + a.experts * 20 + 8;
-  st = ensure_smem(reinterpret_cast<const void*>(situ_nvfp4_gemm_kernel<BN>), smem);
-  if (st != SITU_OK) return st;
-  situ_nvfp4_gemm_kernel<BN><<<grid, P::kThreads, smem, s>>>(ma, mw, a);
-  return check_launch("situ_glu_nvfp4_gemm");
-}
-
-// Clusters of the two-SM kernel that the device holds at once (0: none), asked
-// of the runtime once per device and shared-memory size.
-situ_status_t pair_clusters(cudaLaunchConfig_t* cfg, int* clusters) {
+// Clusters of a kernel that the device holds at once, asked of the runtime once
+// per device, kernel and shared-memory size.
+situ_status_t max_clusters(const void* kernel, cudaLaunchConfig_t* cfg, int* clusters) {
   struct Entry {
     int dev;
+    const void* kernel;
     size_t smem;
     int clusters;
   };
@@ -1203,26 +930,26 @@ situ_status_t pair_clusters(cudaLaunchConfig_t* cfg, int* clusters) {
   if (err != cudaSuccess) return fail(SITU_ERR_CUDA, "cudaGetDevice: %s", cudaGetErrorString(err));
   std::lock_guard<std::mutex> lock(mu);
   for (int i = 0; i < n_seen; ++i)
-    if (seen[i].dev == dev && seen[i].smem == cfg->dynamicSmemBytes) {
+    if (seen[i].dev == dev && seen[i].kernel == kernel && seen[i].smem == cfg->dynamicSmemBytes) {
       *clusters = seen[i].clusters;
       return SITU_OK;
     }
-  err = cudaOccupancyMaxActiveClusters(clusters, reinterpret_cast<const void*>(situ_nvfp4_gemm_pair_kernel), cfg);
-  if (err != cudaSuccess) {
-    (void)cudaGetLastError();  // the query's error is not sticky: the one-SM form runs
-    *clusters = 0;
+  err = cudaOccupancyMaxActiveClusters(clusters, kernel, cfg);
+  if (err != cudaSuccess || *clusters < 1) {
+    (void)cudaGetLastError();  // the query's error is not sticky
+    return fail(SITU_ERR_CUDA, "the device has no room for a cluster of two CTAs: %s", cudaGetErrorString(err));
   }
-  if (n_seen < 64) seen[n_seen++] = {dev, cfg->dynamicSmemBytes, *clusters};
+  if (n_seen < 64) seen[n_seen++] = {dev, kernel, cfg->dynamicSmemBytes, *clusters};
   return SITU_OK;
 }
 
-// Launches the two-SM form; *done is false (and nothing is launched) where the
-// device or the launch cap has no room for a cluster.
-situ_status_t launch_pair(const void* a_data, int64_t a_pitch, const void* w_data, int64_t w_pitch, const Args& a,
-                          cudaStream_t s, bool* done) {
-  *done = false;
-  const int smem = 1024 + kPairSmem + kHeader + a.experts * 20 + 8;
-  situ_status_t st = ensure_smem(reinterpret_cast<const void*>(situ_nvfp4_gemm_pair_kernel), smem);
+template <int BN>
+situ_status_t launch(const void* a_data, int64_t a_pitch, const void* w_data, int64_t w_pitch, const Args& a,
+                     cudaStream_t s) {
+  using P = Shape<BN>;
+  const void* kernel = reinterpret_cast<const void*>(situ_nvfp4_gemm_kernel<BN>);
+  const int smem = 1024 + P::kSmem + kHeader + a.experts * 20 + 8;
+  situ_status_t st = ensure_smem(kernel, smem);
   if (st != SITU_OK) return st;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
@@ -1231,33 +958,34 @@ situ_status_t launch_pair(const void* a_data, int64_t a_pitch, const void* w_dat
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cfg.gridDim = dim3(2, 1, 1);
-  cfg.blockDim = dim3(kPairThreads, 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.dynamicSmemBytes = static_cast<size_t>(smem);
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   int clusters = 0;
-  st = pair_clusters(&cfg, &clusters);
+  st = max_clusters(kernel, &cfg, &clusters);
   if (st != SITU_OK) return st;
   const int cap = g_max_ctas.load(std::memory_order_relaxed);
-  if (cap > 0 && 2 * clusters > cap) clusters = cap / 2;
-  if (clusters == 0) return SITU_OK;
-  const int64_t most = ((a.tokens + kBM2 - 1) / kBM2 + a.experts - 1) * ((a.n + kBN2 - 1) / kBN2);
+  if (cap > 0 && 2 * clusters > cap) clusters = cap < 2 ? 1 : cap / 2;
+  // no more clusters than tiles there can be: every expert may end in a part of one
+  const int64_t most = ((a.tokens + kBM - 1) / kBM + a.experts - 1) * ((a.n + BN - 1) / BN);
   if (clusters > most) clusters = static_cast<int>(most);
   const int64_t w_rows = static_cast<int64_t>(a.experts) * a.n;
-  CUtensorMap ma, mw, mas, mws;
+  CUtensorMap ma, mw, mas = {}, mws = {};
   st = byte_map(&ma, a_data, a.k / 2, a.tokens, a_pitch, kStageRow, 128);
   if (st != SITU_OK) return st;
-  st = byte_map(&mw, w_data, a.k / 2, w_rows, w_pitch, kStageRow, 128);
+  st = byte_map(&mw, w_data, a.k / 2, w_rows, w_pitch, kStageRow, BN / 2);
   if (st != SITU_OK) return st;
-  st = byte_map(&mas, a.a_scale, a.k / 16, a.tokens, a.a_scale_pitch, 64, 128);
-  if (st != SITU_OK) return st;
-  st = byte_map(&mws, a.w_scale, a.k / 16, w_rows, a.w_scale_pitch, 64, kBN2);
-  if (st != SITU_OK) return st;
+  if (a.scale_bytes == 16) {
+    st = byte_map(&mas, a.a_scale, a.k / 16, a.tokens, a.a_scale_pitch, 64, 128);
+    if (st != SITU_OK) return st;
+    st = byte_map(&mws, a.w_scale, a.k / 16, w_rows, a.w_scale_pitch, 64, BN);
+    if (st != SITU_OK) return st;
+  }
   cfg.gridDim = dim3(2 * clusters, 1, 1);
-  const cudaError_t err = cudaLaunchKernelEx(&cfg, situ_nvfp4_gemm_pair_kernel, ma, mw, mas, mws, a);
+  const cudaError_t err = cudaLaunchKernelEx(&cfg, situ_nvfp4_gemm_kernel<BN>, ma, mw, mas, mws, a);
   if (err != cudaSuccess) return fail(SITU_ERR_CUDA, "situ_glu_nvfp4_gemm launch: %s", cudaGetErrorString(err));
-  *done = true;
   return check_launch("situ_glu_nvfp4_gemm");
 }
 
@@ -1440,8 +1168,8 @@ situ_status_t situ_glu_nvfp4_gemm(const void* a_data, int64_t a_data_row_stride,
     return fail(SITU_ERR_UNSUPPORTED, "experts must be in [1, %d], got %lld", nvgemm::kMaxExperts, (long long)experts);
   if (tokens > INT32_MAX - 256 || n > INT32_MAX / experts - 256 || k > INT32_MAX - 256)
     return fail(SITU_ERR_UNSUPPORTED, "sizes exceed the 32-bit tensor-map coordinates");
-  // tiles are numbered in 32 bits (the narrowest have 64 columns)
-  if ((tokens / nvgemm::kBM + experts + 1) > INT32_MAX / (n / 64 + 1))
+  // tiles are numbered in 32 bits (the narrowest have 128 columns)
+  if ((tokens / nvgemm::kBM + experts + 1) > INT32_MAX / (n / 128 + 1))
     return fail(SITU_ERR_UNSUPPORTED, "too many output tiles");
   if (offsets == nullptr && experts != 1) return fail(SITU_ERR_INVALID_ARG, "offsets is NULL with %lld experts", (long long)experts);
   if (a_data_row_stride < k / 2 || a_scale_row_stride < k / 16 || w_data_row_stride < k / 2 ||
@@ -1484,8 +1212,10 @@ situ_status_t situ_glu_nvfp4_gemm(const void* a_data, int64_t a_data_row_stride,
   a.tokens = tokens;
   a.k = static_cast<int>(k);
   a.n = static_cast<int>(n);
-  a.a_vec = aligned(a_scale, 16) && a_scale_row_stride % 16 == 0;
-  a.w_vec = aligned(w_scale, 16) && w_scale_row_stride % 16 == 0;
+  a.scale_bytes = 4;
+  for (int b = 8; b <= 16; b *= 2)
+    if (aligned(a_scale, b) && aligned(w_scale, b) && a_scale_row_stride % b == 0 && w_scale_row_stride % b == 0)
+      a.scale_bytes = b;
   a.out = static_cast<char*>(out);
   a.out_pitch = out_row_stride * oes;
   a.out_bf16 = out_dtype == SITU_DTYPE_BF16;
@@ -1493,20 +1223,13 @@ situ_status_t situ_glu_nvfp4_gemm(const void* a_data, int64_t a_data_row_stride,
   int sms = 0;
   st = device_sm_count(&sms);
   if (st != SITU_OK) return st;
-  // The two-SM form wants full 256-row tiles (an expert's last one is half empty
-  // on average), enough of them for every pair of SMs, and scales that TMA can
-  // read (16-byte aligned rows: k a multiple of 256 where they are contiguous).
-  const int64_t pairs = ((tokens + nvgemm::kBM2 - 1) / nvgemm::kBM2) * ((n + nvgemm::kBN2 - 1) / nvgemm::kBN2);
-  if (2 * pairs >= sms && tokens >= 256 * experts && a.a_vec && a.w_vec) {
-    bool done = false;
-    st = nvgemm::launch_pair(a_data, a_data_row_stride, w_data, w_data_row_stride, a, s, &done);
-    if (st != SITU_OK || done) return st;
-  }
-  // Narrow tiles where wide ones would leave SMs idle (few rows: the weights'
-  // bandwidth is the bound, and more SMs draw more of it).
-  const int64_t wide = ((tokens + nvgemm::kBM - 1) / nvgemm::kBM) * ((n + 191) / 192);
-  if (wide < sms) return nvgemm::launch<64>(a_data, a_data_row_stride, w_data, w_data_row_stride, a, s);
-  return nvgemm::launch<192>(a_data, a_data_row_stride, w_data, w_data_row_stride, a, s);
+  // Tiles of 128 columns where every pair of SMs gets one of them at most (us, 128 and
+  // 256 columns: 512 x 4096 x 4096 11.7, 13.4; 8 x 7168 x 2048 14.0, 16.1); from there
+  // on the wider ones, with fewer operand bytes for the same products (2048 x 7168 x
+  // 2048, 128 narrow tiles: 25.4, 18.3; 1024 x 2048 x 8192: 18.2, 15.1).
+  const int64_t wide = ((tokens + nvgemm::kBM - 1) / nvgemm::kBM + experts - 1) * ((n + 255) / 256);
+  if (4 * wide <= sms) return nvgemm::launch<128>(a_data, a_data_row_stride, w_data, w_data_row_stride, a, s);
+  return nvgemm::launch<256>(a_data, a_data_row_stride, w_data, w_data_row_stride, a, s);
 }
 
 }  // extern "C"

@@ -194,7 +194,7 @@ def product_case(tokens, k, n, offsets, seed, device):
 
 
 # one and several stages of k with whole and part last ones, part tiles of rows and columns, one
-# and many tiles a CTA, narrow (few tiles), wide and two-SM tiles
+# and many tiles a cluster, narrow (few tiles) and wide tiles
 @pytest.mark.parametrize("tokens,k,n", [(1, 64, 8), (1, 256, 64), (3, 128, 72), (128, 256, 64), (129, 320, 192),
                                         (200, 1024, 200), (64, 4160, 136), (1000, 576, 3000), (2500, 512, 1544),
                                         (2600, 768, 1544), (5000, 2304, 1000)])
@@ -220,7 +220,7 @@ def test_groups(offsets, cuda_device):
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("k", [64, 320, 1344])
-def test_groups_of_two_sm_tiles(k, dtype, cuda_device):
+def test_groups_of_wide_tiles(k, dtype, cuda_device):
     offsets = [3, 700, 700, 2990]
     a, w = product_case(3000, k, 1608, offsets, seed=17, device=cuda_device)
     a, w = (a[0], padded(a[1]), a[2]), (w[0], padded(w[1]), w[2])
@@ -235,6 +235,32 @@ def test_groups_of_two_sm_tiles(k, dtype, cuda_device):
     finally:
         abi.situ_glu_set_max_ctas(prev)
     assert abi.situ_glu_device_status(0) == 0
+
+
+@pytest.mark.parametrize("tokens,n,offsets", [(37, 136, [0, 9, 9, 37]), (2900, 1608, [2, 1400, 1403, 2899])])
+def test_alignment_of_the_scales(tokens, n, offsets, cuda_device):
+    """Scales brought by copies of 4 and 8 bytes and by TMA: the same product, whatever lies
+    between and behind the rows."""
+    k = 1344  # rows of 84 bytes of scales
+    a, w = product_case(tokens, k, n, offsets, seed=23, device=cuda_device)
+    off = torch.tensor(offsets, device=cuda_device)
+
+    def pitched(t, pitch, shift):
+        rows = t.numel() // (k // 16)
+        wide = torch.full((rows * pitch + 16,), 0x7F, dtype=torch.uint8, device=cuda_device)  # NaN scales around
+        view = wide[shift:shift + rows * pitch].view(rows, pitch)[:, :k // 16]
+        view.copy_(t.reshape(rows, k // 16).view(torch.uint8))
+        return view.view(*t.shape[:-1], k // 16) if t.dim() == 2 else view.unflatten(0, tuple(t.shape[:-1]))
+
+    results = []
+    for pitch, shift in ((84, 0), (84, 4), (88, 0), (88, 8), (96, 4), (96, 8), (96, 0), (112, 0)):
+        out = torch.full((tokens, n), 3.0, dtype=torch.float32, device=cuda_device)
+        results.append(pkg.situ_glu_nvfp4_gemm((a[0], pitched(a[1], pitch, shift), a[2]),
+                                               (w[0], pitched(w[1], pitch, shift), w[2]), off,
+                                               out_dtype=torch.float32, out=out))
+    check_product(results[0], a, w, offsets, torch.float32)
+    for r in results[1:]:
+        assert torch.equal(r, results[0])
 
 
 def test_offsets_outside_the_rows_are_clamped(cuda_device):
