@@ -16,7 +16,7 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import abi
-from .functional import (DEFAULT_BETA, DEFAULT_LINEAR_BETA, _check_beta, _dtype_code, _given, _mx_buffers, _mx_rule)
+from .functional import (DEFAULT_BETA, DEFAULT_LINEAR_BETA, _check_beta, _dtype_code, _given, _mx_rule)
 
 DEFAULT_EPSILON = 1e-6
 
@@ -62,29 +62,51 @@ def _on(t: torch.Tensor, device, what: str) -> None:
         raise ValueError(f"{what} must be on {device}, got {t.device}")
 
 
+def _all_on(device, *named) -> None:
+    for i in range(0, len(named), 2):
+        if named[i].device != device:
+            _on(named[i], device, named[i + 1])
+
+
 def _matrix(t: torch.Tensor, cols: int):
-    """[..., cols] as [rows, cols] with each row's elements adjacent and rows
-    not overlapping (copied where they are not), and its row pitch."""
-    if t.dim() != 2:
-        t = t.reshape(-1, cols)
+    """[..., cols] as rows of `cols` adjacent elements that do not overlap (copied
+    where they do), and its row pitch.  What is contiguous comes back as it is,
+    of whatever shape."""
     if t.is_contiguous():
         return t, cols
+    if t.dim() != 2:
+        t = t.reshape(-1, cols)
+        if t.is_contiguous():
+            return t, cols
     rows = t.shape[0]
     if t.numel() and (t.stride(1) != 1 or (rows > 1 and t.stride(0) < cols)):
         return t.contiguous(), cols
     return t, t.stride(0) if rows > 1 else cols
 
 
+def _rows(t: torch.Tensor, cols: int) -> int:
+    return t.numel() // cols if cols else 0
+
+
 def _check_eps(eps):
+    if type(eps) is float and 0.0 <= eps < math.inf:
+        return
     if not (isinstance(eps, (int, float)) and math.isfinite(eps) and eps >= 0):
         raise ValueError(f"eps must be a finite number >= 0, got {eps!r}")
+
+
+def _empty(shape, dtype, device):
+    """torch.empty; with its strides given it takes half the host time."""
+    if len(shape) == 2:
+        return torch.empty_strided(shape, (shape[1], 1), dtype=dtype, device=device)
+    return torch.empty(shape, dtype=dtype, device=device)
 
 
 def _out(out, shape, dtype, device, what):
     """A matrix output, allocated when not given: (tensor, its 2-D view, row pitch)."""
     cols = shape[-1]
     if out is None:
-        out = torch.empty(shape, dtype=dtype, device=device)
+        out = _empty(shape, dtype, device)
         return out, out, cols  # contiguous: its rows follow from the pointer and the pitch
     o2 = _given(out, tuple(shape), device, what, dtype)
     return out, o2, o2.stride(0) if o2.shape[0] > 1 else cols
@@ -138,7 +160,7 @@ def situ_glu_rms_norm_fwd(x: torch.Tensor, weight: torch.Tensor, eps: float = DE
             r2, rp = _matrix(residual, hidden)
             h, h2, hp = _out_like(h_out, x, hidden, "h_out")
             r_ptr, h_ptr = r2.data_ptr(), h2.data_ptr()
-        st = abi.situ_glu_rms_norm_fwd(x2.data_ptr(), dtype, x2.shape[0], hidden, xp, r_ptr, rp, w.data_ptr(), wdtype, eps,
+        st = abi.situ_glu_rms_norm_fwd(x2.data_ptr(), dtype, _rows(x2, hidden), hidden, xp, r_ptr, rp, w.data_ptr(), wdtype, eps,
                                        h_ptr, hp, y2.data_ptr(), yp, handle)
     if st:
         abi.check(st, "situ_glu_rms_norm_fwd")
@@ -159,16 +181,16 @@ def situ_glu_rms_norm_fwd_mxfp8(x: torch.Tensor, weight: torch.Tensor, eps: floa
     with _Scope(device, stream) as handle:
         x2, xp = _matrix(x, hidden)
         w = weight.contiguous()
-        data, scale, d2, s2 = _mx_buffers(tuple(x.shape[:-1]), hidden, device, data, scale)
+        lead = tuple(x.shape[:-1])
+        data, d2, dp = _bytes(data, lead + (hidden,), torch.float8_e4m3fn, device, "MXFP8 data")
+        scale, s2, sp = _bytes(scale, lead + (hidden // 32,), torch.uint8, device, "MXFP8 scale")
         h, r_ptr, rp, h_ptr, hp = None, None, 0, None, 0
         if residual is not None:
             r2, rp = _matrix(residual, hidden)
             h, h2, hp = _out_like(h_out, x, hidden, "h_out")
             r_ptr, h_ptr = r2.data_ptr(), h2.data_ptr()
-        rows = x2.shape[0]
-        st = abi.situ_glu_rms_norm_fwd_mxfp8(x2.data_ptr(), dtype, rows, hidden, xp, r_ptr, rp, w.data_ptr(), wdtype, eps,
-                                             h_ptr, hp, d2.data_ptr(), d2.stride(0) if rows > 1 else hidden,
-                                             s2.data_ptr(), s2.stride(0) if rows > 1 else hidden // 32, _mx_rule(rule),
+        st = abi.situ_glu_rms_norm_fwd_mxfp8(x2.data_ptr(), dtype, _rows(x2, hidden), hidden, xp, r_ptr, rp, w.data_ptr(),
+                                             wdtype, eps, h_ptr, hp, d2.data_ptr(), dp, s2.data_ptr(), sp, _mx_rule(rule),
                                              handle)
     if st:
         abi.check(st, "situ_glu_rms_norm_fwd_mxfp8")
@@ -206,12 +228,12 @@ def situ_glu_rms_norm_bwd(grad_y: torch.Tensor, h: torch.Tensor, weight: torch.T
             d_weight = None
         else:
             if d_weight is None:
-                d_weight = torch.empty(hidden, dtype=weight.dtype, device=device)
+                d_weight = torch.empty_strided((hidden,), (1,), dtype=weight.dtype, device=device)
             elif tuple(d_weight.shape) != (hidden,) or d_weight.dtype != weight.dtype or d_weight.device != device or \
                     not d_weight.is_contiguous():
                 raise ValueError(f"d_weight must be a contiguous {weight.dtype} [{hidden}] on {device}")
             dw_ptr = d_weight.data_ptr()
-        tokens = h2.shape[0]
+        tokens = _rows(h2, hidden)
         ws = abi.situ_glu_rms_norm_bwd_workspace_bytes(tokens, hidden, 1) if want_dw else 0
         ws_ptr = None
         if ws:
@@ -227,7 +249,7 @@ def situ_glu_rms_norm_bwd(grad_y: torch.Tensor, h: torch.Tensor, weight: torch.T
 def _workspace(given, nbytes: int, device) -> torch.Tensor:
     """The caller's scratch, or one allocated for this call."""
     if given is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+        return torch.empty_strided((nbytes,), (1,), dtype=torch.uint8, device=device)
     if given.device != device or not given.is_contiguous() or given.numel() * given.element_size() < nbytes:
         raise ValueError(f"workspace must be contiguous, on {device}, of at least {nbytes} bytes")
     return given
@@ -249,12 +271,11 @@ class AddRMSNormFunction(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, grad_y, grad_h=None):
         h, weight = ctx.saved_tensors
-        want_x = ctx.needs_input_grad[0] or ctx.needs_input_grad[3]
-        want_dw = ctx.needs_input_grad[1]
+        needs_x, want_dw, _, needs_residual = ctx.needs_input_grad
         if grad_y is None:  # nothing reached y: the stream's gradient passes through
             return grad_h, torch.zeros_like(weight) if want_dw else None, None, grad_h if ctx.has_residual else None
         d_x, d_w = situ_glu_rms_norm_bwd(grad_y, h, weight, ctx.eps, grad_h=grad_h, want_dw=want_dw)
-        if not want_x:
+        if not (needs_x or needs_residual):
             d_x = None
         return d_x, d_w, None, d_x if ctx.has_residual else None
 
@@ -280,9 +301,8 @@ def situ_glu_moe_fwd(x: torch.Tensor, topk_ids: torch.Tensor, topk_weights: torc
     each (situ_glu_moe_workspace_bytes; allocated when not given)."""
     _check_beta(beta, linear_beta)
     device = _cuda(x, "x")
-    for t, name in ((x, "x"), (w1, "w1"), (w2, "w2")):
-        if t.dtype != torch.bfloat16:
-            raise TypeError(f"{name} must be bfloat16, got {t.dtype}")
+    if not (x.dtype is w1.dtype is w2.dtype is torch.bfloat16):
+        raise TypeError(f"x, w1 and w2 must be bfloat16, got {x.dtype}, {w1.dtype} and {w2.dtype}")
     if x.dim() != 2 or topk_ids.dim() != 2 or topk_ids.shape[0] != x.shape[0]:
         raise ValueError(f"x must be [T, H] and topk_ids [T, k], got {tuple(x.shape)} and {tuple(topk_ids.shape)}")
     if topk_ids.dtype != torch.int64:
@@ -295,8 +315,7 @@ def situ_glu_moe_fwd(x: torch.Tensor, topk_ids: torch.Tensor, topk_weights: torc
     experts, inter = w2.shape[0], w2.shape[2]
     if topk_weights is not None and topk_weights.shape != topk_ids.shape:
         raise ValueError(f"topk_weights must be {tuple(topk_ids.shape)}, got {tuple(topk_weights.shape)}")
-    for t, name in ((topk_ids, "topk_ids"), (w1, "w1"), (w2, "w2")):
-        _on(t, device, name)
+    _all_on(device, topk_ids, "topk_ids", w1, "w1", w2, "w2")
     wdtype = abi.SITU_DTYPE_F32
     if topk_weights is not None:
         _on(topk_weights, device, "topk_weights")
@@ -356,9 +375,9 @@ def situ_glu_nvfp4_quantize(x: torch.Tensor, amax: torch.Tensor | None = None, d
             d_ptr, s_ptr = d2.data_ptr(), s2.data_ptr()
         given = 2 if amax_only else int(amax is not None)
         if amax is None:
-            amax = amax_out if amax_out is not None else torch.empty(1, dtype=torch.float32, device=device)
+            amax = amax_out if amax_out is not None else torch.empty_strided((1,), (1,), dtype=torch.float32, device=device)
         _amax_word(amax, device)
-        st = abi.situ_glu_nvfp4_quantize(x2.data_ptr(), dtype, x2.shape[0], cols, xp, d_ptr, dp, s_ptr, sp, amax.data_ptr(),
+        st = abi.situ_glu_nvfp4_quantize(x2.data_ptr(), dtype, _rows(x2, cols), cols, xp, d_ptr, dp, s_ptr, sp, amax.data_ptr(),
                                          given, handle)
     if st:
         abi.check(st, "situ_glu_nvfp4_quantize")
@@ -394,7 +413,7 @@ def situ_glu_nvfp4_dequantize(data: torch.Tensor, scale: torch.Tensor, amax: tor
         d2, dp = _matrix(data, cols // 2)
         s2, sp = _matrix(scale, cols // 16)
         out, o2, op = _out(out, tuple(data.shape[:-1]) + (cols,), dtype, device, "out")
-        st = abi.situ_glu_nvfp4_dequantize(d2.data_ptr(), dp, s2.data_ptr(), sp, amax.data_ptr(), d2.shape[0], cols,
+        st = abi.situ_glu_nvfp4_dequantize(d2.data_ptr(), dp, s2.data_ptr(), sp, amax.data_ptr(), _rows(o2, cols), cols,
                                            o2.data_ptr(), _dtype_code(out, "out"), op, handle)
     if st:
         abi.check(st, "situ_glu_nvfp4_dequantize")
@@ -418,8 +437,7 @@ def situ_glu_nvfp4_gemm(a, w, offsets: torch.Tensor | None = None, out_dtype: to
     if _codes(wd, wsc, "w") != k or ad.dim() != 2 or wd.dim() not in (2, 3):
         raise ValueError(f"a must hold [T, K] and w [E, N, K] or [N, K], got codes {tuple(ad.shape)} and {tuple(wd.shape)}")
     experts, n = (wd.shape[0], wd.shape[1]) if wd.dim() == 3 else (1, wd.shape[0])
-    for t, name in ((asc, "a's scales"), (wd, "w's codes"), (wsc, "w's scales"), (wa, "w's amax")):
-        _on(t, device, name)
+    _all_on(device, asc, "a's scales", wd, "w's codes", wsc, "w's scales", wa, "w's amax")
     _amax_word(aa, device, "a's amax")
     if wa.dtype != torch.float32 or wa.numel() not in (1, experts):
         raise ValueError(f"w's amax must be 1 or {experts} float32 elements")
@@ -434,7 +452,8 @@ def situ_glu_nvfp4_gemm(a, w, offsets: torch.Tensor | None = None, out_dtype: to
     with _Scope(device, stream) as handle:
         (ad, adp), (asc, asp) = _matrix(ad, k // 2), _matrix(asc, k // 16)
         (wd, wdp), (wsc, wsp) = _matrix(wd, k // 2), _matrix(wsc, k // 16)
-        wa = wa.reshape(-1).contiguous()
+        if not wa.is_contiguous():
+            wa = wa.contiguous()
         off = offsets.contiguous() if offsets is not None else None
         out, o2, op = _out(out, (tokens, n), out_dtype, device, "out")
         st = abi.situ_glu_nvfp4_gemm(ad.data_ptr(), adp, asc.data_ptr(), asp, aa.data_ptr(), tokens, k, wd.data_ptr(), wdp,

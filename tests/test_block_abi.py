@@ -136,7 +136,9 @@ def test_matrix_views_are_copied_only_where_rows_are_not_runs():
     m, pitch = block._matrix(t[:1].expand(4, 12), 12)  # overlapping rows
     assert m.stride(0) == 12 and pitch == 12
     assert block._matrix(t[:0], 12)[0].shape == (0, 12)
-    assert block._matrix(torch.zeros(2, 3, 12), 12)[0].shape == (6, 12)
+    wide = torch.zeros(2, 3, 12)
+    assert block._matrix(wide, 12) == (wide, 12) and block._rows(wide, 12) == 6  # contiguous: as it is
+    assert block._matrix(wide[:, :, :8], 8)[0].shape == (6, 8) and block._rows(wide[:0], 12) == 0
     assert block._matrix(t[1:2, 3:9], 6)[1] == 6  # one row: its pitch is its width
 
 
