@@ -14,7 +14,8 @@
 // one CTA with a contiguous run of units, and one warp streams their rows, a 32
 // KB stage at a time, through a ring with the token rows of the same k: kernel 1
 // multiplies every token of the call (those that are not the expert's cost
-// columns that the product has anyway), kernel 2 the expert's entries.  128 rows
+// columns that the product has anyway), kernel 2 the expert's entries, in one
+// product (64 of them, 7168 x 2048, 8 experts: 164 us, in products of 16 224 us).  128 rows
 // are the tensor cores' tallest product and need the fewest of them, four for 16
 // KB; units of 32 or 64 rows would share out more evenly, but one warp issues
 // twice and four times the products and falls behind HBM.  The SMs that get a
@@ -25,7 +26,7 @@
 // every unit's end (153 / 218 us); staged in shared memory and multiplied with
 // mma.sync, the warps' loads of the token rows wait behind the ring's copies, and
 // with those staged too the eight warps take longer over a stage than HBM does
-// (139 / 224 us).  This one takes 131 / 172 us, 5.4 and 4.7 TB/s of weights.
+// (139 / 224 us).  This one takes 128 / 154 us, 5.5 and 5.2 TB/s of weights.
 //
 // Which tokens an expert has is worked out by every CTA from the token's
 // choices: a 64-bit token mask per expert, and a running count over the
@@ -60,7 +61,7 @@ constexpr int kMoeWeightBytes = kMoeChunks * kMoeTileBytes;       // of a stage
 constexpr int kMoeTile = 16;                         // entries of one product of kernel 2 (32 columns)
 constexpr int kMoeMaxStages = 8;
 constexpr int kMoeTmemCols = 256;                    // two accumulators of 128
-constexpr int kMoeSmem = 224 * 1024;
+constexpr int kMoeSmem = 227 * 1024;
 
 struct MoeArgs {
   const int64_t* ids;
@@ -83,12 +84,11 @@ struct MoePlan {
   float weight[kMoeMaxEntries];             // of each entry
   uint16_t start[kMoeMaxExperts + 1];       // first entry of each expert
   uint16_t active[kMoeMaxEntries];          // experts that have a token, rising
-  int16_t id[kMoeMaxEntries];               // [token][choice], -1: none or named before
-  uint8_t token[kMoeMaxEntries];            // of each entry
-  float up[2][16][64];                      // kernel 1: the up halves of 16 tokens, for the gate halves' warps
+  int16_t id[kMoeMaxEntries];               // [token][choice] its expert, then its entry; -1: none or named before
   int complete[128];                        // kernel 2: column groups whose experts are all done
   int warp_active[kMoeThreads / 32], warp_entries[kMoeThreads / 32];
-  int n_active;
+  int n_active, most;                       // most: entries of the expert that has the most
+  float up[2][16][64];                      // kernel 1: the up halves of 16 tokens, for the gate halves' warps
 };
 
 __device__ __forceinline__ int64_t moe_id(const MoeArgs& a, int t, int j) {
@@ -99,6 +99,7 @@ __device__ __forceinline__ int64_t moe_id(const MoeArgs& a, int t, int j) {
 __device__ __forceinline__ void moe_plan(const MoeArgs& a, MoePlan& p) {
   const int n = a.tokens * a.topk;
   for (int e = threadIdx.x; e < a.experts; e += kMoeThreads) p.mask[e] = 0;
+  if (threadIdx.x == 0) p.most = 0;
   __syncthreads();
   for (int i = threadIdx.x; i < n; i += kMoeThreads) {
     const int t = i / a.topk, j = i - t * a.topk;
@@ -113,12 +114,15 @@ __device__ __forceinline__ void moe_plan(const MoeArgs& a, MoePlan& p) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int per = (a.experts + kMoeThreads - 1) / kMoeThreads;
   const int e0 = min(a.experts, static_cast<int>(threadIdx.x) * per), e1 = min(a.experts, e0 + per);
-  int act = 0, ent = 0;
+  int act = 0, ent = 0, most = 0;
   for (int e = e0; e < e1; ++e) {
     const int c = __popcll(p.mask[e]);
     act += c > 0;
     ent += c;
+    most = max(most, c);
   }
+  most = __reduce_max_sync(0xffffffffu, most);
+  if (lane == 0) atomicMax(&p.most, most);
   int act_incl = act, ent_incl = ent;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -154,7 +158,7 @@ __device__ __forceinline__ void moe_plan(const MoeArgs& a, MoePlan& p) {
     if (id < 0) continue;
     const int t = i / a.topk;
     const int entry = p.start[id] + __popcll(p.mask[id] & ((1ull << t) - 1));
-    p.token[entry] = static_cast<uint8_t>(t);
+    p.id[i] = static_cast<int16_t>(entry);
     float w = 0.0f;
     for (int j = 0; j < a.topk; ++j) {
       if (moe_id(a, t, j) != id) continue;
@@ -212,18 +216,22 @@ __device__ __forceinline__ int moe_first(int units, int i, int grid) {
   return static_cast<int>(static_cast<int64_t>(units) * i / grid);
 }
 
-constexpr int kMoeTail = (256 + sizeof(MoePlan) + 1023) / 1024 * 1024;  // barriers and plan, after the ring
+// The ring, before barriers and plan (whose last member kernel 2 does without).
+__host__ __device__ constexpr int moe_ring(bool fc2) {
+  const int tail = 256 + static_cast<int>(fc2 ? offsetof(MoePlan, up) : sizeof(MoePlan));
+  return kMoeSmem - 1024 - (tail + 1023) / 1024 * 1024;
+}
 
-// Columns of kernel 1's product: the call's tokens; of kernel 2's largest: two
-// per entry.
-__host__ __device__ constexpr int moe_columns(int tokens, bool fc2) {
-  return (tokens + kMoeTile - 1) / kMoeTile * kMoeTile * (fc2 ? 2 : 1);
+// Columns of kernel 1's product: the call's tokens; of kernel 2's largest: two per
+// entry of the expert that has the most, which the plan knows.
+__host__ __device__ constexpr int moe_columns(int entries, bool fc2) {
+  return (entries + kMoeTile - 1) / kMoeTile * kMoeTile * (fc2 ? 2 : 1);
 }
-__host__ __device__ constexpr int moe_stage_bytes(int tokens, bool fc2) {
-  return kMoeWeightBytes + moe_columns(tokens, fc2) * kMoeChunk * 2 * kMoeChunks;
+__host__ __device__ constexpr int moe_stage_bytes(int entries, bool fc2) {
+  return kMoeWeightBytes + moe_columns(entries, fc2) * kMoeChunk * 2 * kMoeChunks;
 }
-__host__ __device__ constexpr int moe_stages(int tokens, bool fc2) {
-  const int s = (kMoeSmem - 1024 - kMoeTail) / moe_stage_bytes(tokens, fc2);
+__host__ __device__ constexpr int moe_stages(int entries, bool fc2) {
+  const int s = moe_ring(fc2) / moe_stage_bytes(entries, fc2);
   return s < kMoeMaxStages ? s : kMoeMaxStages;
 }
 static_assert(moe_stages(kMoeMaxTokens, true) >= 3, "the ring is too short");
@@ -251,14 +259,43 @@ __device__ __forceinline__ MoeSmem moe_smem(unsigned char* raw, int ring_bytes) 
   return m;
 }
 
+// Columns col .. col + 3 of y: warp q's tokens q, q + 4, ..., TOKENS of them and 16
+// of their rows at a time, so that as many loads are in flight.  The CTA that completes
+// a group of columns is among the last to end, and all the others wait for it (4096 x
+// 1024, 64 slots, top 4 of 32: 171 us with the loads of one token in flight, 154 us
+// with eight tokens'; for one token eight would be mostly idle work, 125 and 129 us).
+template <int TOKENS>
+__device__ __forceinline__ void moe_sum(const MoeArgs& a, const MoePlan& plan, int col, int q) {
+  constexpr int kUnroll = 16 / TOKENS;
+  for (int t0 = q; t0 < a.tokens; t0 += 4 * TOKENS) {
+    float4 s[TOKENS];
+#pragma unroll
+    for (int n = 0; n < TOKENS; ++n) s[n] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll kUnroll
+    for (int j = 0; j < a.topk; ++j) {
+#pragma unroll
+      for (int n = 0; n < TOKENS; ++n) {
+        const int t = t0 + 4 * n, entry = t < a.tokens ? plan.id[t * a.topk + j] : -1;
+        const float4 p =
+            __ldcg(reinterpret_cast<const float4*>(a.part + static_cast<int64_t>(entry >= 0 ? entry : 0) * a.hidden + col));
+        if (entry >= 0) s[n].x += p.x, s[n].y += p.y, s[n].z += p.z, s[n].w += p.w;
+      }
+    }
+#pragma unroll
+    for (int n = 0; n < TOKENS; ++n)
+      if (t0 + 4 * n < a.tokens)
+        *reinterpret_cast<uint2*>(a.y + (t0 + 4 * n) * a.y_pitch + col * 2) =
+            make_uint2(Bf16::pack(make_float2(s[n].x, s[n].y)), Bf16::pack(make_float2(s[n].z, s[n].w)));
+  }
+}
+
 // Both kernels: FC2 false is W1 with the activation, true W2 with the sums.
 template <bool FC2, int GATE, bool HAS_LB>
 __global__ void __launch_bounds__(kMoeThreads, 1)
     situ_moe_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ CUtensorMap tmap_b,
                     const MoeArgs a) {
   extern __shared__ unsigned char smem_raw[];
-  const int stages = moe_stages(a.tokens, FC2), stage_bytes = moe_stage_bytes(a.tokens, FC2);
-  const MoeSmem m = moe_smem(smem_raw, stages * stage_bytes);
+  const MoeSmem m = moe_smem(smem_raw, moe_ring(FC2));
   const MoePlan& plan = *m.plan;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if constexpr (!FC2) {
@@ -288,6 +325,8 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
   moe_plan(a, *m.plan);
   fc1::tc_fence_after();
   const uint32_t tmem = *m.tmem_slot;
+  const int widest = FC2 ? plan.most : a.tokens;
+  const int stages = moe_stages(widest, FC2), stage_bytes = moe_stage_bytes(widest, FC2);
 
   // Kernel 1: expert by expert.  Kernel 2: column group by column group, every expert.
   const int n_active = plan.n_active, k = FC2 ? a.inter : a.hidden;
@@ -333,8 +372,10 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
     auto columns = [&](const Unit& v, int step, int st) {
       const uint32_t at = m.ring + st * stage_bytes + kMoeWeightBytes;
       if constexpr (FC2) {
-        for (int i = 0; i < v.tiles; ++i)
-          moe_box(at + i * tile_bytes, &tmap_b, 2 * (v.start + i * kMoeTile), step * kMoeChunks, &m.full[st]);
+        for (int c = 0; c < kMoeChunks; ++c)  // a chunk's columns of all the expert's entries side by side
+          for (int i = 0; i < v.tiles; ++i)
+            moe_box(at + (c * v.tiles + i) * (tile_bytes / kMoeChunks), &tmap_b, 2 * (v.start + i * kMoeTile),
+                    step * kMoeChunks + c, &m.full[st]);
       } else {
         moe_box(at, &tmap_b, 0, step * kMoeChunks, &m.full[st]);
       }
@@ -388,8 +429,6 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
         if (issued & (1u << s)) mbar_wait(&m.full[s], s < stage ? phase : phase ^ 1u);
   } else if (warp == 1) {
     // ---- products ----
-    const int n_cols = FC2 ? 2 * kMoeTile : moe_columns(a.tokens, false);
-    const uint32_t idesc = moe_idesc(n_cols);
     int stage = 0, it = 0;
     uint32_t phase = 0, acc_phase = 0;
     bool ok = true;
@@ -401,7 +440,9 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
       }
       fc1::tc_fence_after();
       const uint32_t d = tmem + static_cast<uint32_t>(b * (kMoeTmemCols / 2));
-      const int n_tiles = FC2 ? unit(u).tiles : 1;
+      const int n_cols = FC2 ? unit(u).tiles * 2 * kMoeTile : moe_columns(a.tokens, false);
+      const uint32_t idesc = moe_idesc(n_cols);
+      const uint64_t t_chunk = n_cols * (kMoeChunk * 2 / 16);
       for (int step = 0; step < steps; ++step) {
         if (!fc1::wait_or_abort(&m.full[stage], phase, m.abort_flag)) {
           ok = false;
@@ -410,17 +451,13 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
         fc1::tc_fence_after();
         const uint32_t at = m.ring + stage * stage_bytes;
         const uint64_t w = fc1::smem_desc_sw128(at);
-        uint64_t t = fc1::smem_desc_sw128(at + kMoeWeightBytes);
-        const uint64_t t_chunk = FC2 ? 2 * kMoeTile * kMoeChunk * 2 / 16 : n_cols * (kMoeChunk * 2 / 16);
-        for (int i = 0; i < n_tiles; ++i, t += tile_bytes / 16) {
-          const uint32_t di = d + i * 2 * kMoeTile;
+        const uint64_t t = fc1::smem_desc_sw128(at + kMoeWeightBytes);
 #pragma unroll
-          for (int c = 0; c < kMoeChunks; ++c)
+        for (int c = 0; c < kMoeChunks; ++c)
 #pragma unroll
-            for (int s = 0; s < 4; ++s)
-              moe_mma(di, w + (c * kMoeTileBytes + s * 32) / 16, t + c * t_chunk + s * 2, idesc,
-                      (step | c | s) != 0 ? 1u : 0u, lane == 0);
-        }
+          for (int s = 0; s < 4; ++s)
+            moe_mma(d, w + (c * kMoeTileBytes + s * 32) / 16, t + c * t_chunk + s * 2, idesc,
+                    (step | c | s) != 0 ? 1u : 0u, lane == 0);
         if (lane == 0) fc1::umma_commit(&m.empty[stage]);
         __syncwarp();
         if (++stage == stages) {
@@ -530,23 +567,13 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
           }
           asm volatile("bar.sync 1, 128;" ::: "memory");
           __threadfence();
-          // thread: four columns of every fourth token
-          const int col4 = (thread & 31) * 4;
           for (int gi = 0; gi < some; ++gi) {
-            const int col = (b0 + base + gi) * kMoeRows + col4;
+            const int col = (b0 + base + gi) * kMoeRows + (thread & 31) * 4;
             if (!plan.complete[gi] || col >= a.hidden) continue;
-            for (int tok = thread >> 5; tok < a.tokens; tok += 4) {
-              float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-              for (int j = 0; j < a.topk; ++j) {
-                const int id = plan.id[tok * a.topk + j], e = id >= 0 ? id : 0;
-                const int entry = id >= 0 ? plan.start[e] + __popcll(plan.mask[e] & ((1ull << tok) - 1)) : 0;
-                const float4 p = __ldcg(reinterpret_cast<const float4*>(a.part + static_cast<int64_t>(entry) * a.hidden + col));
-                if (id >= 0) s.x += p.x, s.y += p.y, s.z += p.z, s.w += p.w;
-              }
-              *reinterpret_cast<uint2*>(a.y + tok * a.y_pitch + col * 2) =
-                  make_uint2(Bf16::pack(make_float2(s.x, s.y)), Bf16::pack(make_float2(s.z, s.w)));
-            }
+            if (a.tokens > 16)
+              moe_sum<8>(a, plan, col, thread >> 5);
+            else
+              moe_sum<2>(a, plan, col, thread >> 5);
           }
           asm volatile("bar.sync 1, 128;" ::: "memory");
         }
@@ -614,7 +641,7 @@ situ_status_t launch_moe(const MoeArgs& a, const MoeCall& c, cudaStream_t s) {
   if (st != SITU_OK) return st;
   st = moe_map(&mw2, c.w2, c.experts * a.hidden, a.inter, c.w2_stride, kMoeRows, kMoeChunks);
   if (st != SITU_OK) return st;
-  st = moe_map(&ma, a.act, static_cast<int64_t>(a.tokens) * a.topk * 2, a.inter, a.inter, 2 * kMoeTile, kMoeChunks);
+  st = moe_map(&ma, a.act, static_cast<int64_t>(a.tokens) * a.topk * 2, a.inter, a.inter, 2 * kMoeTile, 1);
   if (st != SITU_OK) return st;
   const MoeKernel k1 = c.lb ? pick_moe_fc1<true>(c.gate) : pick_moe_fc1<false>(c.gate);
   const MoeKernel k2 = situ_moe_kernel<true, kGateGeneric, false>;
