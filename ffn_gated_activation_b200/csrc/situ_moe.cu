@@ -14,8 +14,7 @@
 // one CTA with a contiguous run of units, and one warp streams their rows, a 32
 // KB stage at a time, through a ring with the token rows of the same k: kernel 1
 // multiplies every token of the call (those that are not the expert's cost
-// columns that the product has anyway), kernel 2 the expert's entries, in one
-// product (64 of them, 7168 x 2048, 8 experts: 164 us, in products of 16 224 us).  128 rows
+// columns that the product has anyway), kernel 2 the expert's entries.  128 rows
 // are the tensor cores' tallest product and need the fewest of them, four for 16
 // KB; units of 32 or 64 rows would share out more evenly, but one warp issues
 // twice and four times the products and falls behind HBM.  The SMs that get a
@@ -58,7 +57,7 @@ constexpr int kMoeRows = 128;                        // weight rows of a unit
 constexpr int kMoeChunks = 2;                        // of a stage
 constexpr int kMoeTileBytes = kMoeRows * kMoeChunk * 2;           // one chunk's weights
 constexpr int kMoeWeightBytes = kMoeChunks * kMoeTileBytes;       // of a stage
-constexpr int kMoeTile = 16;                         // entries of one product of kernel 2 (32 columns)
+constexpr int kMoeTile = 16;                         // entries of one box of kernel 2 (32 columns)
 constexpr int kMoeMaxStages = 8;
 constexpr int kMoeTmemCols = 256;                    // two accumulators of 128
 constexpr int kMoeSmem = 227 * 1024;

@@ -306,7 +306,10 @@ __global__ void __launch_bounds__(kStoreThreads) situ_nvfp4_quantize_kernel(cons
 }
 
 // A small matrix in one launch: a cluster of eight CTAs finds A, exchanges it
-// through shared memory and quantises what it has just read (from L2).
+// through shared memory and quantises what it has just read (from L2).  Against a
+// fill and two launches (bf16, us in a graph): 7168 blocks 3.6, 6.2; 16576 5.6, 6.2;
+// 33152 8.3, 6.2.  Call by call, where the host is the bound, 13.3 and 17.0 up to
+// 49280 blocks; the limit lies between the two.
 constexpr int kSmallCtas = 8, kSmallThreads = 1024;
 constexpr int64_t kSmallBlocks = 32768;  // blocks of 16
 template <typename S>
@@ -1143,10 +1146,17 @@ situ_status_t situ_glu_nvfp4_dequantize(const void* data, int64_t data_row_strid
   fill_store(&a, rows, cols,
              rows == 1 || (out_row_stride == cols && data_row_stride == cols / 2 && scale_row_stride == cols / 16));
   auto k = dtype == SITU_DTYPE_BF16 ? situ_nvfp4_dequantize_kernel<Bf16> : situ_nvfp4_dequantize_kernel<F32>;
+  // Two blocks a thread, as many CTAs as that takes: their turnover overlaps one's
+  // stores with the next one's loads (bf16 57344 x 2048: 45 us, a loop of resident CTAs
+  // 50 us).
+  const int64_t ctas = (a.blocks + 2 * kStoreThreads - 1) / (2 * kStoreThreads);
   int grid = 0;
-  st = launch_grid(reinterpret_cast<const void*>(k), kStoreThreads, 0, (a.blocks + kStoreThreads - 1) / kStoreThreads,
-                   &grid);
-  if (st != SITU_OK) return st;
+  if (g_max_ctas.load(std::memory_order_relaxed) <= 0 && ctas <= INT32_MAX) {
+    grid = static_cast<int>(ctas);
+  } else {
+    st = launch_grid(reinterpret_cast<const void*>(k), kStoreThreads, 0, ctas, &grid);
+    if (st != SITU_OK) return st;
+  }
   k<<<grid, kStoreThreads, 0, static_cast<cudaStream_t>(stream)>>>(a);
   return check_launch("situ_glu_nvfp4_dequantize");
 }
