@@ -570,7 +570,8 @@ situ_status_t situ_glu_nvfp4_dequantize(const void *data, int64_t data_row_strid
  * k a multiple of 64, n of 8, experts in [1, 1024] (SITU_ERR_UNSUPPORTED otherwise);
  * data 16-byte aligned with pitches of a multiple of 16, scales 4-byte aligned with
  * pitches of a multiple of 4, out 16-byte aligned with a row pitch of a multiple of
- * 16 bytes.  A scale of 0x7F (NaN) makes its output rows or columns NaN.  tokens == 0
+ * 16 bytes.  Scales whose rows all start on 16 bytes (k a multiple of 256, or a padded
+ * pitch) are read fastest.  A scale of 0x7F (NaN) makes its output rows or columns NaN.  tokens == 0
  * launches nothing.  Every internal wait is bounded (situ_glu_device_status). */
 situ_status_t situ_glu_nvfp4_gemm(const void *a_data, int64_t a_data_row_stride,
                                   const void *a_scale, int64_t a_scale_row_stride, const float *a_amax,
@@ -593,8 +594,10 @@ int situ_glu_abi_version(void);
 
 /* Upper bound on the CTAs of each launch (0 = automatic: SM count times the
  * CTAs per SM the occupancy calculator allows).  Results do not depend on it;
- * it exists for tuning and to check that.  Process-wide; returns the previous
- * value, or -1 (and changes nothing) for a negative argument. */
+ * it exists for tuning and to check that.  A kernel that works in clusters of CTAs
+ * (the NVFP4 product, the quantisation of a small matrix) runs one cluster at least.
+ * Process-wide; returns the previous value, or -1 (and changes nothing) for a
+ * negative argument. */
 int situ_glu_set_max_ctas(int max_ctas);
 
 /* How the kernels read HBM.  0 (default): every thread loads its own 16-byte

@@ -270,12 +270,12 @@ def test_offsets_outside_the_rows_are_clamped(cuda_device):
     check_product(out, a, w, [0, 40, 100], torch.float32)
 
 
-def test_many_experts(cuda_device):
-    experts = 70
+@pytest.mark.parametrize("experts,k,n", [(70, 192, 40), (1024, 64, 8)])  # 1024: the most there may be
+def test_many_experts(experts, k, n, cuda_device):
     cuts = torch.sort(torch.randint(0, 401, (experts - 1,), generator=torch.Generator().manual_seed(2)))[0]
     offsets = [0, *cuts.tolist(), 400]
-    a, w = product_case(400, 192, 40, offsets, seed=9, device=cuda_device)
-    out = torch.full((400, 40), 3.0, dtype=torch.bfloat16, device=cuda_device)
+    a, w = product_case(400, k, n, offsets, seed=9, device=cuda_device)
+    out = torch.full((400, n), 3.0, dtype=torch.bfloat16, device=cuda_device)
     pkg.situ_glu_nvfp4_gemm(a, w, torch.tensor(offsets, device=cuda_device), out=out)
     check_product(out, a, w, offsets, torch.bfloat16)
 
