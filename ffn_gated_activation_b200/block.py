@@ -283,7 +283,11 @@ class AddRMSNormFunction(torch.autograd.Function):
 def add_rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = DEFAULT_EPSILON,
                  residual: torch.Tensor | None = None):
     """Differentiable residual addition + RMS norm over the last axis: y, or
-    (y, h) with a residual (h = x + residual, the residual stream from here on)."""
+    (y, h) with a residual (h = x + residual, the residual stream from here on).
+    As with any PyTorch function, a step captured into a CUDA graph whose
+    backward() accumulates into leaves' .grad must not share these leaves with an
+    eager graph that is still alive: drop that one first, or use
+    torch.autograd.grad."""
     return AddRMSNormFunction.apply(x, weight, eps, residual)
 
 
