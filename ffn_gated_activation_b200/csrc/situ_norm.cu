@@ -176,10 +176,10 @@ __global__ void __launch_bounds__(kNormThreads<V, MX>) situ_rms_norm_fwd_kernel(
 
 // Chunks by the row's width: enough for the CTAs (or, in narrow rows, the warps)
 // that share an SM, few enough that the partial rows stay a few per cent of the
-// traffic.
+// traffic (bf16 3000 x 16384: 117 us with 148 chunks, 124 with twice as many).
 constexpr int kNormMaxChunks = 2368;
 int64_t norm_chunks(int64_t tokens, int64_t hidden) {
-  const int64_t most = hidden <= 1024 ? kNormMaxChunks : hidden <= 4096 ? 592 : 296;
+  const int64_t most = hidden <= 1024 ? kNormMaxChunks : hidden <= 4096 ? 592 : 148;
   return tokens < most ? tokens : most;
 }
 

@@ -471,7 +471,7 @@ situ_status_t situ_glu_rms_norm_bwd(const void *grad_y, int64_t grad_y_row_strid
                                     void *workspace, size_t workspace_bytes, void *stream);
 
 /* Bytes of workspace situ_glu_rms_norm_bwd needs: one fp32 row of partial sums
- * per chunk of rows (at most 296 chunks, 592 for hidden <= 4096, 2368 for
+ * per chunk of rows (at most 148 chunks, 592 for hidden <= 4096, 2368 for
  * hidden <= 1024) when want_dweight != 0, else 0. */
 size_t situ_glu_rms_norm_bwd_workspace_bytes(int64_t tokens, int64_t hidden, int want_dweight);
 

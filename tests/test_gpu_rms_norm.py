@@ -10,7 +10,7 @@ half(t) the storage type's (bf16 2^-8, fp32 2^-24), both relative.
   * d_x: the same sums bound each of its terms relative to the terms' sizes, so
     64 u of |grad_h| + |q g| + |h| q^3 mean |g h| covers them.
   * d_weight: terms that are each within 32 u.  The rows of one of the C chunks
-    (C = T up to 2368, 592 or 296 by the row's width) are added in order, ceil(T / C)
+    (C = T up to 2368, 592 or 148 by the row's width) are added in order, ceil(T / C)
     additions; then the chunks in 1024 / 8 groups, ceil(C / 128) + 32 + 4 additions, or
     in 1024 / 32 groups, ceil(C / 32) + 32.  ceil(T / C) + ceil(C / 32) + 36 covers both.
 """
@@ -47,7 +47,7 @@ def close(got, ref, bound, what):
 
 def dw_bound(tokens, hidden):
     """d_weight's additions and its terms' error, in u of the sum of magnitudes."""
-    chunks = min(tokens, 2368 if hidden <= 1024 else 592 if hidden <= 4096 else 296)
+    chunks = min(tokens, 2368 if hidden <= 1024 else 592 if hidden <= 4096 else 148)
     return (-(-tokens // chunks) + -(-chunks // 32) + 36 + 32) * U
 
 
