@@ -218,22 +218,38 @@ __global__ void __launch_bounds__(kNormThreads<V>) situ_rms_norm_bwd_kernel(cons
     if constexpr (kInSmem) return dw_smem[(i * S::kPairs + p) * nt + threadIdx.x];
     else return dw_reg[i][p];
   };
+  // The next row's vectors are loaded while this one is summed, up to two vectors a
+  // thread (bf16 60000 x 256: 26 us, without 32; 40000 x 512: 28, 33); three or four
+  // take the registers of other warps (40000 x 768: 51, without 45).
+  constexpr bool kAhead = V <= 2;
+  auto load = [&](int64_t row, auto& h, auto& g, auto& gh) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int j = threadIdx.x + i * nt;
+      if (j < a.vpr) {
+        if (kEarly && a.gh != nullptr)
+          gh[kEarly ? i : 0] = ld_stream(a.gh + row * a.gh_pitch + static_cast<int64_t>(j) * kVecBytes);
+        h[i] = ld_stream(a.h + row * a.h_pitch + static_cast<int64_t>(j) * kVecBytes);
+        g[i] = ld_stream(a.gy + row * a.gy_pitch + static_cast<int64_t>(j) * kVecBytes);
+      }
+    }
+  };
   for (int64_t c = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y; c < a.chunks;
        c += static_cast<int64_t>(gridDim.x) * blockDim.y) {
 #pragma unroll
     for (int i = 0; i < V; ++i)
 #pragma unroll
       for (int p = 0; p < S::kPairs; ++p) dw(i, p) = make_float2(0.0f, 0.0f);
+    uint4 next_h[kAhead ? V : 1], next_g[kAhead ? V : 1], next_gh[kAhead ? V : 1];
+    if constexpr (kAhead) load(c, next_h, next_g, next_gh);
     for (int64_t row = c; row < a.tokens; row += a.chunks) {
       uint4 h[V], g[V], gh[kEarly ? V : 1];
+      if constexpr (kAhead) {
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const int j = threadIdx.x + i * nt;
-        if (j < a.vpr) {
-          if (kEarly && a.gh != nullptr) gh[i] = ld_stream(a.gh + row * a.gh_pitch + static_cast<int64_t>(j) * kVecBytes);
-          h[i] = ld_stream(a.h + row * a.h_pitch + static_cast<int64_t>(j) * kVecBytes);
-          g[i] = ld_stream(a.gy + row * a.gy_pitch + static_cast<int64_t>(j) * kVecBytes);
-        }
+        for (int i = 0; i < V; ++i) h[i] = next_h[i], g[i] = next_g[i], gh[i] = next_gh[i];
+        if (row + a.chunks < a.tokens) load(row + a.chunks, next_h, next_g, next_gh);
+      } else {
+        load(row, h, g, gh);
       }
       float2 ss = make_float2(0.0f, 0.0f), gd = ss;
 #pragma unroll
@@ -802,7 +818,7 @@ situ_status_t situ_glu_rms_norm_bwd(const void* grad_y, int64_t grad_y_row_strid
   const bool bf = dtype == SITU_DTYPE_BF16;
   // Staged rows from 129 vectors up to 2048, of which two or more fit in shared
   // memory.  Narrower rows have a warp each and enough of them in flight (bf16 65536 x
-  // 1024: 92 us, staged 96; 40000 x 512: 37, staged 48); wider ones gain from the ring
+  // 1024: 92 us, staged 96; 40000 x 512: 33, staged 48); wider ones gain from the ring
   // (32768 x 2048: 97 us, direct 105; 8191 x 4096: 51, direct 60).
   if (a.vpr > 128 && a.vpr <= 2048) {
     st = launch_norm_ring(a, bf, s);
