@@ -148,9 +148,15 @@ def situ_glu_rms_norm_fwd(x: torch.Tensor, weight: torch.Tensor, eps: float = DE
     """h = x + residual (rounded to x's dtype), y = h / sqrt(mean h^2 + eps) * weight
     over the last axis of x [..., hidden].  Returns (y, h); h is None without a
     residual.  ``weight`` [hidden] in bf16 or fp32; y and h in x's dtype."""
-    device, dtype, wdtype, hidden = _norm_args(x, weight, eps, residual)
+    args = _norm_args(x, weight, eps, residual)
     if residual is None and h_out is not None:
         raise ValueError("h_out needs a residual")
+    return _norm_fwd(args, x, weight, eps, residual, out, h_out, stream)
+
+
+def _norm_fwd(args, x, weight, eps, residual, out, h_out, stream):
+    """situ_glu_rms_norm_fwd after its checks; ``args`` as _norm_args returns them."""
+    device, dtype, wdtype, hidden = args
     with _Scope(device, stream) as handle:
         x2, xp = _matrix(x, hidden)
         w = weight.contiguous()
@@ -207,13 +213,20 @@ def situ_glu_rms_norm_bwd(grad_y: torch.Tensor, h: torch.Tensor, weight: torch.T
     stream's).  d_weight is summed in fp32 in an order that the shape fixes.
     Calls that overlap on the GPU need a ``workspace`` each
     (situ_glu_rms_norm_bwd_workspace_bytes; allocated when not given)."""
-    device, dtype, wdtype, hidden = _norm_args(h, weight, eps, None)
+    args = _norm_args(h, weight, eps, None)
+    device = args[0]
     for name, g in (("grad_y", grad_y), ("grad_h", grad_h)):
         if g is not None:
             if g.shape != h.shape or g.dtype != h.dtype:
                 raise ValueError(f"{name} must have h's shape {tuple(h.shape)} and dtype {h.dtype}, got "
                                  f"{tuple(g.shape)} {g.dtype}")
             _on(g, device, name)
+    return _norm_bwd(args, grad_y, h, weight, eps, grad_h, want_dw, d_x, d_weight, workspace, stream)
+
+
+def _norm_bwd(args, grad_y, h, weight, eps, grad_h, want_dw, d_x=None, d_weight=None, workspace=None, stream=None):
+    """situ_glu_rms_norm_bwd after its checks."""
+    device, dtype, wdtype, hidden = args
     with _Scope(device, stream) as handle:
         h2, hp = _matrix(h, hidden)
         g2, gp = _matrix(grad_y, hidden)
@@ -261,23 +274,33 @@ class AddRMSNormFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, eps, residual):
         ctx.set_materialize_grads(False)
-        y, h = situ_glu_rms_norm_fwd(x, weight, eps, residual)
-        ctx.eps = eps
-        ctx.has_residual = residual is not None
-        ctx.save_for_backward(h if residual is not None else x, weight)
-        return (y, h) if residual is not None else y
+        args = _norm_args(x, weight, eps, residual)
+        y, h = _norm_fwd(args, x, weight, eps, residual, None, None, None)
+        ctx.args, ctx.eps = args, eps
+        if residual is None:
+            ctx.save_for_backward(x, weight)
+            return y
+        ctx.save_for_backward(h, weight)
+        return y, h
 
     @staticmethod
-    @once_differentiable
     def backward(ctx, grad_y, grad_h=None):
-        h, weight = ctx.saved_tensors
-        needs_x, want_dw, _, needs_residual = ctx.needs_input_grad
-        if grad_y is None:  # nothing reached y: the stream's gradient passes through
-            return grad_h, torch.zeros_like(weight) if want_dw else None, None, grad_h if ctx.has_residual else None
-        d_x, d_w = situ_glu_rms_norm_bwd(grad_y, h, weight, ctx.eps, grad_h=grad_h, want_dw=want_dw)
-        if not (needs_x or needs_residual):
-            d_x = None
-        return d_x, d_w, None, d_x if ctx.has_residual else None
+        # (the wrapper that makes a second derivative an error costs a few
+        # microseconds, and is needed only where one may follow)
+        return _norm_grads_once(ctx, grad_y, grad_h) if torch.is_grad_enabled() else _norm_grads(ctx, grad_y, grad_h)
+
+
+def _norm_grads(ctx, grad_y, grad_h):
+    needs_x, want_dw, _, needs_residual = ctx.needs_input_grad
+    h, weight = ctx.saved_tensors
+    if grad_y is None:  # nothing reached y: the stream's gradient passes through
+        d_x, d_w = grad_h, torch.zeros_like(weight) if want_dw else None
+    else:  # the engine has checked the gradients' shapes, types and devices
+        d_x, d_w = _norm_bwd(ctx.args, grad_y, h, weight, ctx.eps, grad_h, want_dw)
+    return d_x if needs_x else None, d_w, None, d_x if needs_residual else None
+
+
+_norm_grads_once = once_differentiable(_norm_grads)
 
 
 def add_rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = DEFAULT_EPSILON,

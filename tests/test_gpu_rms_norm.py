@@ -217,3 +217,11 @@ def test_autograd_forms(cuda_device):
     y.backward(torch.ones_like(y))
     dx, dw = pkg.situ_glu_rms_norm_bwd(torch.ones_like(x), h.detach(), w, EPS)
     assert torch.equal(a.grad, dx) and torch.equal(wl.grad, dw)
+
+
+def test_a_second_derivative_is_an_error(cuda_device):
+    x = make(torch.float32, 3, 64, 91).to(cuda_device).requires_grad_(True)
+    w = torch.ones(64, device=cuda_device, requires_grad=True)
+    (dx,) = torch.autograd.grad(pkg.add_rms_norm(x, w, EPS).square().sum(), (x,), create_graph=True)
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        dx.sum().backward()
