@@ -316,6 +316,7 @@ template <typename S>
 __global__ void __cluster_dims__(kSmallCtas, 1, 1) __launch_bounds__(kSmallThreads) situ_nvfp4_small_kernel(const StoreArgs a) {
   __shared__ unsigned int warp_max[kSmallThreads / 32];
   __shared__ unsigned int cta_max[kSmallCtas];
+  cluster_started();  // waited for before the first store to another CTA
   const int64_t first = static_cast<int64_t>(blockIdx.x) * kSmallThreads + threadIdx.x, step = kSmallCtas * kSmallThreads;
   int64_t row;
   int64_t col;
@@ -328,6 +329,7 @@ __global__ void __cluster_dims__(kSmallCtas, 1, 1) __launch_bounds__(kSmallThrea
   const unsigned int bits = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
   if ((threadIdx.x & 31) == 0) warp_max[threadIdx.x >> 5] = bits;
   __syncthreads();
+  cluster_wait_started();
   if (threadIdx.x < 32) {
     const unsigned int most = __reduce_max_sync(0xffffffffu, warp_max[threadIdx.x]);
     if (threadIdx.x < kSmallCtas)  // into slot `rank` of CTA threadIdx.x

@@ -1,0 +1,37 @@
+"""Quantisation of small matrices, which one cluster of CTAs does in one launch:
+its CTAs exchange their maxima, those without a block of their own among them."""
+import pytest
+import torch
+
+import ffn_gated_activation_b200 as pkg
+
+from test_gpu_nvfp4_product import check_codes, make
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows,cols", [(1, 16), (1, 32), (3, 16), (1, 16 * 1024), (2, 16 * 1024), (9, 16 * 1000)])
+def test_maxima_of_a_cluster(rows, cols, dtype, cuda_device):
+    """The maximum in the last, the first and a middle block, one to all eight CTAs having blocks."""
+    for seed, at in enumerate((0, rows * cols // 2, rows * cols - 1)):
+        x = make(dtype, rows, cols, seed=seed)
+        x.view(-1)[at] = -9.0 - seed
+        data, scale, amax = pkg.situ_glu_nvfp4_quantize(x.to(cuda_device))
+        assert float(amax) == 9.0 + seed
+        check_codes(x, data, scale, amax)
+
+
+def test_many_clusters_in_flight(cuda_device):
+    """Many calls side by side, so that a cluster's CTAs start while others end: each its own maximum."""
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    xs = [make(torch.bfloat16, 1, 16, seed=i).to(cuda_device) for i in range(64)]
+    alone = [float(x.abs().max()) for x in xs]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(25):
+        got += [(i, pkg.situ_glu_nvfp4_quantize(x, stream=streams[i % 4])) for i, x in enumerate(xs)]
+    torch.cuda.synchronize()
+    assert all(float(q[2]) == alone[i] for i, q in got)
+    for i in range(64):
+        check_codes(xs[i].cpu(), *got[-64 + i][1])
