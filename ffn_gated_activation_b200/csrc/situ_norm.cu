@@ -95,6 +95,15 @@ __device__ __forceinline__ float2 row_sum2(float2 v, float2* slot, int warps) {
   return make_float2(warp_sum(p.x), warp_sum(p.y));
 }
 
+// A row whose mean square (with epsilon) leaves [kMeanLow, kMeanHigh] has squares
+// that fp32 does not hold, or not to its precision.  Its threads, which see the same
+// mean, sum it once more with every element times a power of two that brings them
+// all into range: the largest element of a small row to at most 2^58, the largest
+// fp32 number to 2^48 (16384 squares add 14 bits), the smallest to 2^-49.
+constexpr float kMeanLow = 0x1p-100f, kMeanHigh = 0x1p120f;
+__device__ __forceinline__ bool mean_in_range(float mean) { return mean >= kMeanLow && mean <= kMeanHigh; }
+__device__ __forceinline__ float range_scale(float mean) { return mean < kMeanLow ? 0x1p100f : 0x1p-80f; }
+
 // h = x + r in the storage type.
 template <typename S>
 __device__ __forceinline__ uint4 add_vec(const uint4& x, const uint4& r) {
@@ -139,9 +148,27 @@ __global__ void __launch_bounds__(kNormThreads<V, MX>) situ_rms_norm_fwd_kernel(
         }
       }
     }
-    const float ss = row_sum(acc.x + acc.y, slots[flip], warps);
+    const float mean = row_sum(acc.x + acc.y, slots[flip], warps) * a.inv_hidden + a.eps;
     flip ^= 1;
-    const float q = rsqrtf(ss * a.inv_hidden + a.eps);
+    float q = rsqrtf(mean);
+    if (!mean_in_range(mean)) {
+      const float s = range_scale(mean);
+      acc = make_float2(0.0f, 0.0f);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        if (static_cast<int>(threadIdx.x) + i * nt < a.vpr) {
+#pragma unroll
+          for (int p = 0; p < S::kPairs; ++p) {
+            const float2 f = mul2(as_f2(S::pair(h[i], p)), splat(s));
+            acc = fma2(f, f, acc);
+            if (s > 1.0f) S::put(h[i], p, f);  // exact; 1 / rms itself may leave fp32
+          }
+        }
+      }
+      q = rsqrtf(row_sum(acc.x + acc.y, slots[flip], warps) * a.inv_hidden + a.eps * s * s);
+      flip ^= 1;
+      if (s < 1.0f) q *= s;
+    }
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int j = threadIdx.x + i * nt;
