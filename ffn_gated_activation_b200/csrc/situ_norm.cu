@@ -12,6 +12,7 @@
 // per thread, thread t holding vectors t, t + n, ... of the row.
 
 #include <initializer_list>
+#include <type_traits>
 
 #include "situ_host.cuh"
 
@@ -95,14 +96,47 @@ __device__ __forceinline__ float2 row_sum2(float2 v, float2* slot, int warps) {
   return make_float2(warp_sum(p.x), warp_sum(p.y));
 }
 
-// A row whose mean square (with epsilon) leaves [kMeanLow, kMeanHigh] has squares
-// that fp32 does not hold, or not to its precision.  Its threads, which see the same
-// mean, sum it once more with every element times a power of two that brings them
-// all into range: the largest element of a small row to at most 2^58, the largest
-// fp32 number to 2^48 (16384 squares add 14 bits), the smallest to 2^-49.
-constexpr float kMeanLow = 0x1p-100f, kMeanHigh = 0x1p120f;
+// A row whose mean square (with epsilon) leaves [kMeanLow, kMeanHigh] has squares, or
+// products with powers of 1 / rms, that fp32 does not hold or not to its precision.  Its
+// threads, which see the same mean, sum it once more with every element times a power
+// of two that brings them all into range: the squares of a small row to at most 2^114
+// in all, of the largest fp32 numbers to 2^110 (16384 of them), and the smallest
+// element to 2^-59.
+constexpr float kMeanLow = 0x1p-80f, kMeanHigh = 0x1p80f;
 __device__ __forceinline__ bool mean_in_range(float mean) { return mean >= kMeanLow && mean <= kMeanHigh; }
-__device__ __forceinline__ float range_scale(float mean) { return mean < kMeanLow ? 0x1p100f : 0x1p-80f; }
+__device__ __forceinline__ float range_scale(float mean) { return mean < kMeanLow ? 0x1p90f : 0x1p-80f; }
+
+// What the backward needs of a row, from sums = (sum h^2, sum g h):
+//   q       1 / rms
+//   along   d_x = q g + along h,        along = -q q (q mean(g h))      of ordinary rows
+//           d_x = q g + along (h q),    along = -q (q mean(g h))        of rows out of range,
+// whose q q fp32 may not hold.  `lift`: the sums' h is the row's times it.
+struct RowScale {
+  float q, along;
+  bool far;  // the mean is out of range
+};
+template <bool ONE_FORM = false>  // the second form for every row
+__device__ __forceinline__ RowScale row_scale(const float2& sums, float mean, float inv_hidden) {
+  const float q = rsqrtf(mean), t = q * (sums.y * inv_hidden);
+  return {q, ONE_FORM ? -q * t : -q * (q * t), !mean_in_range(mean)};
+}
+__device__ __forceinline__ RowScale far_row_scale(const float2& sums, float inv_hidden, float eps, float lift) {
+  const float u = rsqrtf(sums.x * inv_hidden + eps * lift * lift), q = u * lift;
+  return {q, -q * (u * (sums.y * inv_hidden)), true};
+}
+// A pair of d_x (without grad_h) and of the terms of d_weight.
+template <bool FAR>
+__device__ __forceinline__ float2 norm_grad(const RowScale& k, const float2& h, const float2& g, const float2& w, float2& dw) {
+  if constexpr (FAR) {
+    const float2 n = mul2(h, splat(k.q));
+    dw = fma2(g, n, dw);
+    return fma2(mul2(g, splat(k.q)), w, mul2(n, splat(k.along)));
+  } else {
+    const float2 gq = mul2(g, splat(k.q));
+    dw = fma2(gq, h, dw);
+    return fma2(gq, w, mul2(h, splat(k.along)));
+  }
+}
 
 // h = x + r in the storage type.
 template <typename S>
@@ -228,6 +262,27 @@ struct NormBwdArgs {
   float eps, inv_hidden;
 };
 
+// The sums of a row of which this thread has the vectors h and g, with h times s.
+template <typename S, int V>
+__device__ __forceinline__ float2 far_sums(const NormBwdArgs& a, int nt, const uint4 (&h)[V], const uint4 (&g)[V], float s) {
+  float2 ss = make_float2(0.0f, 0.0f), gd = ss;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int j = threadIdx.x + i * nt;
+    if (j < a.vpr) {
+      float2 w[S::kPairs];
+      norm_weights<S>(a.w, a.w_bf16, j, w);
+#pragma unroll
+      for (int p = 0; p < S::kPairs; ++p) {
+        const float2 f = mul2(as_f2(S::pair(h[i], p)), splat(s));
+        ss = fma2(f, f, ss);
+        gd = fma2(mul2(as_f2(S::pair(g[i], p)), w[p]), f, gd);
+      }
+    }
+  }
+  return make_float2(ss.x + ss.y, gd.x + gd.y);
+}
+
 template <typename S, int V>
 __global__ void __launch_bounds__(kNormThreads<V>) situ_rms_norm_bwd_kernel(const NormBwdArgs a) {
   __shared__ float2 slots[2][32];
@@ -295,29 +350,35 @@ __global__ void __launch_bounds__(kNormThreads<V>) situ_rms_norm_bwd_kernel(cons
       }
       const float2 sums = row_sum2(make_float2(ss.x + ss.y, gd.x + gd.y), slots[flip], warps);
       flip ^= 1;
-      const float q = rsqrtf(sums.x * a.inv_hidden + a.eps);
-      const float along = -(q * q * q) * (sums.y * a.inv_hidden);
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const int j = threadIdx.x + i * nt;
-        if (j < a.vpr) {
-          uint4 o;
-          if (!kEarly && a.gh != nullptr) gh[0] = ld_stream(a.gh + row * a.gh_pitch + static_cast<int64_t>(j) * kVecBytes);
-          const uint4& ghi = gh[kEarly ? i : 0];
-          float2 w[S::kPairs];
-          norm_weights<S>(a.w, a.w_bf16, j, w);
-#pragma unroll
-          for (int p = 0; p < S::kPairs; ++p) {
-            const float2 f = as_f2(S::pair(h[i], p));
-            const float2 gq = mul2(as_f2(S::pair(g[i], p)), splat(q));
-            float2 d = fma2(gq, w[p], mul2(f, splat(along)));
-            if (a.gh != nullptr) d = add2(d, as_f2(S::pair(ghi, p)));
-            S::put(o, p, d);
-            dw(i, p) = fma2(gq, f, dw(i, p));
-          }
-          st_stream(a.dx + row * a.dx_pitch + static_cast<int64_t>(j) * kVecBytes, o);
-        }
+      const float mean = sums.x * a.inv_hidden + a.eps;
+      RowScale k = row_scale(sums, mean, a.inv_hidden);
+      if (k.far) {
+        const float lift = range_scale(mean);
+        k = far_row_scale(row_sum2(far_sums<S>(a, nt, h, g, lift), slots[flip], warps), a.inv_hidden, a.eps, lift);
+        flip ^= 1;
       }
+      auto finish = [&](auto far) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          const int j = threadIdx.x + i * nt;
+          if (j < a.vpr) {
+            uint4 o;
+            if (!kEarly && a.gh != nullptr) gh[0] = ld_stream(a.gh + row * a.gh_pitch + static_cast<int64_t>(j) * kVecBytes);
+            const uint4& ghi = gh[kEarly ? i : 0];
+            float2 w[S::kPairs];
+            norm_weights<S>(a.w, a.w_bf16, j, w);
+#pragma unroll
+            for (int p = 0; p < S::kPairs; ++p) {
+              float2 d = norm_grad<far.value>(k, as_f2(S::pair(h[i], p)), as_f2(S::pair(g[i], p)), w[p], dw(i, p));
+              if (a.gh != nullptr) d = add2(d, as_f2(S::pair(ghi, p)));
+              S::put(o, p, d);
+            }
+            st_stream(a.dx + row * a.dx_pitch + static_cast<int64_t>(j) * kVecBytes, o);
+          }
+        }
+      };
+      if (k.far) finish(std::true_type{});
+      else finish(std::false_type{});
     }
     if (a.partials != nullptr) {
       float* out = a.partials + c * (static_cast<int64_t>(a.vpr) * 2 * S::kPairs);
@@ -345,8 +406,15 @@ struct NormRing {
   int stage_bytes;
 };
 
+// The registers of the narrow rows' four CTAs an SM are asked for where the compiler
+// would take more (bf16 32768 x 2048 with three: 108 us, four 98 us); two of 544
+// threads have as many as four of 288.
+template <int V>
+constexpr int kRingThreads = V == 1 ? 288 : 544;
 template <typename S, int V, bool GH>
-__global__ void __launch_bounds__(544) situ_rms_norm_bwd_ring_kernel(const NormBwdArgs a, const NormRing r) {
+constexpr int kRingCtas = V == 1 ? 4 : V == 2 && S::kPairs == 2 && !GH ? 2 : 0;
+template <typename S, int V, bool GH>
+__global__ void __launch_bounds__(kRingThreads<V>, kRingCtas<S, V, GH>) situ_rms_norm_bwd_ring_kernel(const NormBwdArgs a, const NormRing r) {
   extern __shared__ __align__(128) unsigned char ring[];
   __shared__ float2 slots[2][32];
   __shared__ uint64_t full[8], empty[8];
@@ -410,6 +478,10 @@ __global__ void __launch_bounds__(544) situ_rms_norm_bwd_ring_kernel(const NormB
       norm_weights<S>(a.w, a.w_bf16, threadIdx.x + i * nt, w);
     }
   };
+  // Rows of one vector a thread have the registers for both forms of the outputs (bf16
+  // 32768 x 2048 without grad_h: 77 us, with the second form alone 79 us); wider ones
+  // lose more to the other loop's (3000 x 16384 without: 100 us, with both 110 us).
+  constexpr bool kOneForm = V > 1;
   int flip = 0;
   bool dead = false;  // a wait expired: the control flow goes on, without waits
   for (int64_t c = blockIdx.x; c < a.chunks; c += gridDim.x) {
@@ -456,27 +528,33 @@ __global__ void __launch_bounds__(544) situ_rms_norm_bwd_ring_kernel(const NormB
       }
       const float2 sums = row_sum2<1>(make_float2(ss.x + ss.y, gd.x + gd.y), slots[flip], warps);
       flip ^= 1;
-      const float q = rsqrtf(sums.x * a.inv_hidden + a.eps);
-      const float along = -(q * q * q) * (sums.y * a.inv_hidden);
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const int j = threadIdx.x + i * nt;
-        if (j < a.vpr) {
-          uint4 o;
-          float2 w[S::kPairs];
-          weights(i, w);
-#pragma unroll
-          for (int p = 0; p < S::kPairs; ++p) {
-            const float2 f = as_f2(S::pair(h[i], p));
-            const float2 gq = mul2(as_f2(S::pair(g[i], p)), splat(q));
-            float2 d = fma2(gq, w[p], mul2(f, splat(along)));
-            if (GH) d = add2(d, as_f2(S::pair(gh[i], p)));
-            S::put(o, p, d);
-            dw[i][p] = fma2(gq, f, dw[i][p]);
-          }
-          st_stream(a.dx + row * a.dx_pitch + static_cast<int64_t>(j) * kVecBytes, o);
-        }
+      const float mean = sums.x * a.inv_hidden + a.eps;
+      RowScale k = row_scale<kOneForm>(sums, mean, a.inv_hidden);
+      if (k.far) {
+        const float lift = range_scale(mean);
+        k = far_row_scale(row_sum2<1>(far_sums<S>(a, nt, h, g, lift), slots[flip], warps), a.inv_hidden, a.eps, lift);
+        flip ^= 1;
       }
+      auto finish = [&](auto far) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          const int j = threadIdx.x + i * nt;
+          if (j < a.vpr) {
+            uint4 o;
+            float2 w[S::kPairs];
+            weights(i, w);
+#pragma unroll
+            for (int p = 0; p < S::kPairs; ++p) {
+              float2 d = norm_grad<far.value>(k, as_f2(S::pair(h[i], p)), as_f2(S::pair(g[i], p)), w[p], dw[i][p]);
+              if (GH) d = add2(d, as_f2(S::pair(gh[i], p)));
+              S::put(o, p, d);
+            }
+            st_stream(a.dx + row * a.dx_pitch + static_cast<int64_t>(j) * kVecBytes, o);
+          }
+        }
+      };
+      if (kOneForm || k.far) finish(std::true_type{});
+      else finish(std::false_type{});
     }
     if (a.partials != nullptr) {
       float* out = a.partials + c * (static_cast<int64_t>(a.vpr) * 2 * S::kPairs);

@@ -62,3 +62,36 @@ def test_mxfp8(dtype, hidden, powers, eps, cuda_device):
     ref = (ref_unit(x, eps) * w.double()).numpy()
     parity.check_mx("rms_norm mxfp8", codes.cpu().view(torch.uint8).numpy(), scale.cpu().numpy(), ref, 33 * U * np.abs(ref),
                     abi.SITU_MX_RULE_OCP)
+
+
+@pytest.mark.parametrize("dtype,power", [(torch.bfloat16, -131), (torch.float32, -131), (torch.float32, -141)])
+def test_rows_of_subnormal_numbers(dtype, power, cuda_device):
+    """1 / rms is above fp32's largest number; the normalised row is not."""
+    for hidden in (128, 2056, 16384):
+        x = rows_of(dtype, hidden, (power, power), 5)
+        y, _ = pkg.situ_glu_rms_norm_fwd(x.to(cuda_device), torch.ones(hidden, device=cuda_device), 0.0)
+        ref = ref_unit(x, 0.0)
+        close(y, ref, (HALF[dtype] + 33 * U) * ref.abs(), "y")
+
+
+# the direct kernels (a warp; eight vectors a thread), the staged one with one, two and four vectors a thread
+@pytest.mark.parametrize("powers,eps", [(LARGE, 1e-6), (LARGE, 0.0), (SMALL, 0.0), (SMALL, 2.0 ** -110)])
+@pytest.mark.parametrize("dtype,hidden", WIDTHS + [(torch.bfloat16, 1544), (torch.bfloat16, 512), (torch.bfloat16, 768),
+                                                   (torch.float32, 516), (torch.float32, 4100), (torch.float32, 256)])
+def test_backward(dtype, hidden, powers, eps, cuda_device):
+    """d_x within 64 u of its terms' sizes and one rounding, d_weight within its terms' 33 u
+    and its additions' (two dozen rows: a chunk each, one join of 36 additions)."""
+    h, w = rows_of(dtype, hidden, powers, 6), weight_of(hidden, 7)
+    gy, gh = make(dtype, h.shape[0], hidden, 8), make(dtype, h.shape[0], hidden, 9)
+    unit, g = ref_unit(h, eps), gy.double() * w.double()
+    q = 1 / torch.sqrt(h.double().square().mean(-1, keepdim=True) + eps)
+    along = unit * (g * unit).mean(-1, keepdim=True)
+    size = q * (g.abs() + unit.abs() * (g * unit).abs().mean(-1, keepdim=True))
+    terms = gy.double() * unit
+    for grad_h in (None, gh):
+        dx, dw = pkg.situ_glu_rms_norm_bwd(gy.to(cuda_device), h.to(cuda_device), w.to(cuda_device), eps,
+                                           grad_h=grad_h.to(cuda_device) if grad_h is not None else None)
+        more = grad_h.double() if grad_h is not None else torch.zeros_like(unit)
+        ref = more + q * (g - along)
+        close(dx, ref, HALF[dtype] * ref.abs() + 64 * U * (size + more.abs()) + SMALLEST[dtype], "d_x")
+        close(dw, terms.sum(0), U * terms.sum(0).abs() + (33 + 40) * U * terms.abs().sum(0), "d_weight")
