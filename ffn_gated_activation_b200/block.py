@@ -16,7 +16,7 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import abi
-from .functional import (DEFAULT_BETA, DEFAULT_LINEAR_BETA, _check_beta, _dtype_code, _given, _mx_rule)
+from .functional import (DEFAULT_BETA, DEFAULT_LINEAR_BETA, _check_beta, _dtype_code, _given, _mx_rule, aligned_rows)
 
 DEFAULT_EPSILON = 1e-6
 
@@ -295,7 +295,10 @@ def _norm_grads(ctx, grad_y, grad_h):
     h, weight = ctx.saved_tensors
     if grad_y is None:  # nothing reached y: the stream's gradient passes through
         d_x, d_w = grad_h, torch.zeros_like(weight) if want_dw else None
-    else:  # the engine has checked the gradients' shapes, types and devices
+    else:  # the engine has checked the gradients' shapes, types and devices, not their alignment
+        grad_y = aligned_rows(grad_y)
+        if grad_h is not None:
+            grad_h = aligned_rows(grad_h)
         d_x, d_w = _norm_bwd(ctx.args, grad_y, h, weight, ctx.eps, grad_h, want_dw)
     return d_x if needs_x else None, d_w, None, d_x if needs_residual else None
 

@@ -53,6 +53,19 @@ def _rows(gate_up: torch.Tensor):
     return g2, lead, inter
 
 
+def aligned_rows(t: torch.Tensor) -> torch.Tensor:
+    """t [..., cols], cols a multiple of 16 bytes, or a copy of it where a row does not
+    start on 16 bytes: for gradients, whose layout the autograd engine chooses
+    (those of torch.cat's parts are slices of a wider one)."""
+    if t.data_ptr() % 16 == 0:
+        if t.is_contiguous():
+            return t
+        size = t.element_size()
+        if all(s * size % 16 == 0 for s, n in zip(t.stride()[:-1], t.shape) if n > 1):
+            return t
+    return t.clone(memory_format=torch.contiguous_format)
+
+
 def _given(t: torch.Tensor, shape: tuple, device, what: str, dtype=None) -> torch.Tensor:
     """A caller's output buffer, checked before the library writes to it (the
     library sees a pointer and a row pitch only, so a smaller or strided
