@@ -644,7 +644,7 @@ class WeightedSiTUFunction(torch.autograd.Function):
         gate_up = saved[0]
         rw = saved[1] if ctx.has_rw else None
         want_drw = ctx.has_rw and ctx.needs_input_grad[1]
-        d_gate_up, d_rw = situ_glu_bwd(gate_up, rw, grad_out, ctx.beta, ctx.linear_beta,
+        d_gate_up, d_rw = situ_glu_bwd(gate_up, rw, aligned_rows(grad_out), ctx.beta, ctx.linear_beta,
                                        want_drw=want_drw)
         return d_gate_up, d_rw, None, None
 

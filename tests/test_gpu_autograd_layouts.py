@@ -46,3 +46,19 @@ def test_norm_gradients_at_odd_offsets(cuda_device):
         dx, dw = torch.autograd.grad(y, (x, w), g, retain_graph=True)
         want = pkg.situ_glu_rms_norm_bwd(g.clone(), x.detach(), w.detach(), EPS)
         assert torch.equal(dx, want[0]) and torch.equal(dw, want[1])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("weights", ["row", "col", None])
+def test_activation_concatenated_with_a_few_columns(weights, dtype, cuda_device):
+    x = normal(9, 2 * 136, seed=6, dtype=dtype, device=cuda_device).requires_grad_(True)
+    w = {"row": torch.rand(9, 1), "col": torch.rand(136), None: None}[weights]
+    w = w.to(cuda_device).requires_grad_(True) if w is not None else None
+    for before, after in ((0, 4), (3, 1)):
+        g = normal(9, 136 + before + after, seed=7, dtype=dtype, device=cuda_device)
+        pad = [torch.zeros(9, n, dtype=dtype, device=cuda_device) for n in (before, after)]
+        y = pkg.weighted_situ(x, w)
+        got = torch.autograd.grad(torch.cat((pad[0], y, pad[1]), -1), [t for t in (x, w) if t is not None], g)
+        cut = g[:, before:before + 136].clone(memory_format=torch.contiguous_format)
+        dx, dw = pkg.situ_glu_bwd(x.detach(), w.detach() if w is not None else None, cut)
+        assert torch.equal(got[0], dx) and (w is None or torch.equal(got[1], dw))
