@@ -13,7 +13,6 @@ import contextlib
 import math
 
 import torch
-from torch.autograd.function import once_differentiable
 
 from . import abi
 from .functional import (DEFAULT_BETA, DEFAULT_LINEAR_BETA, _check_beta, _dtype_code, _given, _mx_rule, aligned_rows)
@@ -285,9 +284,28 @@ class AddRMSNormFunction(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, grad_y, grad_h=None):
-        # (the wrapper that makes a second derivative an error costs a few
-        # microseconds, and is needed only where one may follow)
-        return _norm_grads_once(ctx, grad_y, grad_h) if torch.is_grad_enabled() else _norm_grads(ctx, grad_y, grad_h)
+        if not torch.is_grad_enabled():
+            return _norm_grads(ctx, grad_y, grad_h)
+        with torch.no_grad():  # create_graph: a second derivative may follow
+            grads = _norm_grads(ctx, grad_y, grad_h)
+        anchor = next(t for t in ctx.saved_tensors if t.requires_grad)
+        given = [g for g in grads if g is not None]
+        guarded = iter(_OnceDifferentiable.apply(anchor, *given))
+        return tuple(g if g is None else next(guarded) for g in grads)
+
+
+class _OnceDifferentiable(torch.autograd.Function):
+    """Gradients as they are, whose own derivative is an error.  They depend on the
+    norm's inputs (``anchor`` stands for these) even where the gradients that came
+    in are constants, so that nothing else would tell that it is missing."""
+
+    @staticmethod
+    def forward(ctx, anchor, *grads):
+        return tuple(g.view_as(g) for g in grads)
+
+    @staticmethod
+    def backward(ctx, *grads):
+        raise RuntimeError("add_rms_norm is once_differentiable: it has no second derivative")
 
 
 def _norm_grads(ctx, grad_y, grad_h):
@@ -301,9 +319,6 @@ def _norm_grads(ctx, grad_y, grad_h):
             grad_h = aligned_rows(grad_h)
         d_x, d_w = _norm_bwd(ctx.args, grad_y, h, weight, ctx.eps, grad_h, want_dw)
     return d_x if needs_x else None, d_w, None, d_x if needs_residual else None
-
-
-_norm_grads_once = once_differentiable(_norm_grads)
 
 
 def add_rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = DEFAULT_EPSILON,
