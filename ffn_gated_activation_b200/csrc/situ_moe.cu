@@ -180,6 +180,11 @@ __device__ __forceinline__ void put_split(__nv_bfloat16* out, int apart, float v
   out[apart] = __float2bfloat16(isfinite(rest) ? rest : 0.0f);
 }
 
+// The two columns' products as one.  The values' column alone says what an infinite or
+// NaN weight gives: times a remainder, which may be 0 or of the other sign, it says
+// something else.
+__device__ __forceinline__ float join_split(float value, float rest) { return isfinite(value) ? value + rest : value; }
+
 // A box of rows of k elements [k0, ...): [chunk of 64 elements][row][128 bytes],
 // the 16-byte pieces of a row swizzled by the row.
 __device__ __forceinline__ void moe_box(uint32_t dst, const CUtensorMap* map, int32_t row, int32_t chunk, uint64_t* bar) {
@@ -501,7 +506,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
 #pragma unroll
           for (int j = 0; j < 8; ++j)
             if (in && i + j < v.count)
-              out[static_cast<int64_t>(i + j) * a.hidden] = __uint_as_float(r[2 * j]) + __uint_as_float(r[2 * j + 1]);
+              out[static_cast<int64_t>(i + j) * a.hidden] = join_split(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
           __syncwarp();
         }
       } else {
