@@ -224,7 +224,24 @@ struct TensorScale {
   }
 };
 
-template <typename S, bool EXACT>
+// bf16 elements to +-cap, so that no product below is infinite and the residual of a
+// saturated element keeps its sign.
+__device__ __forceinline__ void clamp_block(uint4 (&v)[2], float cap) {
+  const __nv_bfloat162 hi = __float2bfloat162_rn(cap), lo = __hneg2(hi);
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    uint32_t* w = reinterpret_cast<uint32_t*>(&v[k]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      __nv_bfloat162 x = *reinterpret_cast<__nv_bfloat162*>(&w[i]);
+      x = __hmax2(__hmin2(x, hi), lo);
+      w[i] = *reinterpret_cast<uint32_t*>(&x);
+    }
+  }
+}
+
+// GIVEN: elements may lie above A.
+template <typename S, bool EXACT, bool GIVEN>
 __device__ __forceinline__ void quantize_block(const StoreArgs& a, const TensorScale& t, int64_t row, int64_t col,
                                                uint4 (&v)[8 / S::kPairs]) {
   const float m = block_max<S>(v);
@@ -240,6 +257,9 @@ __device__ __forceinline__ void quantize_block(const StoreArgs& a, const TensorS
     const float s = e4m3_value(sc);
     const float inv = s > 0.0f ? __fdividef(t.s_enc, s) : 0.0f;  // 2 ulp
     if constexpr (EXACT) {
+      if constexpr (GIVEN && S::kPairs == 4) {
+        if (m * inv > 16.0f) clamp_block(v, 16.0f / inv);  // far beyond the largest code, 6
+      }
       const float2 d = splat(-(t.big * s)), r = splat(inv), r1 = splat(inv * (1.0f / 2688.0f));
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -277,7 +297,7 @@ __device__ __forceinline__ void quantize_block(const StoreArgs& a, const TensorS
 
 // Blocks [0, blocks) from the end: what the pass before read last may still be in
 // L2; a thread's next block is on its way while this one is coded.
-template <typename S, bool EXACT>
+template <typename S, bool EXACT, bool GIVEN>
 __device__ __forceinline__ void quantize_blocks(const StoreArgs& a, const TensorScale& t, int64_t k, int64_t step) {
   int64_t row, next_row, col, next_col;
   if (k >= a.blocks) return;
@@ -287,7 +307,7 @@ __device__ __forceinline__ void quantize_blocks(const StoreArgs& a, const Tensor
     k += step;
     const bool more = k < a.blocks;
     if (more) get_block<S>(a, a.blocks - 1 - k, next_row, next_col, next);
-    quantize_block<S, EXACT>(a, t, row, col, v);
+    quantize_block<S, EXACT, GIVEN>(a, t, row, col, v);
     if (!more) break;
 #pragma unroll
     for (int i = 0; i < 8 / S::kPairs; ++i) v[i] = next[i];
@@ -296,13 +316,13 @@ __device__ __forceinline__ void quantize_blocks(const StoreArgs& a, const Tensor
   }
 }
 
-template <typename S>
+template <typename S, bool GIVEN>
 __global__ void __launch_bounds__(kStoreThreads) situ_nvfp4_quantize_kernel(const StoreArgs a) {
   const TensorScale t(*a.amax);
   const int64_t first = static_cast<int64_t>(blockIdx.x) * kStoreThreads + threadIdx.x;
   const int64_t step = static_cast<int64_t>(gridDim.x) * kStoreThreads;
-  if (std::is_same<S, Bf16>::value && t.short_big) quantize_blocks<S, true>(a, t, first, step);
-  else quantize_blocks<S, false>(a, t, first, step);
+  if (std::is_same<S, Bf16>::value && t.short_big) quantize_blocks<S, true, GIVEN>(a, t, first, step);
+  else quantize_blocks<S, false, GIVEN>(a, t, first, step);
 }
 
 // A small matrix in one launch: a cluster of eight CTAs finds A, exchanges it
@@ -343,8 +363,8 @@ __global__ void __cluster_dims__(kSmallCtas, 1, 1) __launch_bounds__(kSmallThrea
   const float amax = __uint_as_float(most);
   if (first == 0) *reinterpret_cast<float*>(a.amax_out) = amax;
   const TensorScale t(amax);
-  if (std::is_same<S, Bf16>::value && t.short_big) quantize_blocks<S, true>(a, t, first, step);
-  else quantize_blocks<S, false>(a, t, first, step);
+  if (std::is_same<S, Bf16>::value && t.short_big) quantize_blocks<S, true, false>(a, t, first, step);
+  else quantize_blocks<S, false, false>(a, t, first, step);
 }
 
 // Two E2M1 codes as an exact half2.
@@ -1108,7 +1128,8 @@ situ_status_t situ_glu_nvfp4_quantize(const void* x, situ_dtype_t dtype, int64_t
     st = check_launch("situ_glu_nvfp4_quantize (amax)");
     if (st != SITU_OK || only) return st;
   }
-  auto k = bf ? situ_nvfp4_quantize_kernel<Bf16> : situ_nvfp4_quantize_kernel<F32>;
+  auto k = bf ? (amax_given != 0 ? situ_nvfp4_quantize_kernel<Bf16, true> : situ_nvfp4_quantize_kernel<Bf16, false>)
+              : situ_nvfp4_quantize_kernel<F32, false>;  // whose codes saturate whatever A is
   st = launch_grid(reinterpret_cast<const void*>(k), kStoreThreads, 0, ctas, &grid);
   if (st != SITU_OK) return st;
   k<<<grid, kStoreThreads, 0, s>>>(a);

@@ -35,3 +35,18 @@ def test_many_clusters_in_flight(cuda_device):
     assert all(float(q[2]) == alone[i] for i, q in got)
     for i in range(64):
         check_codes(xs[i].cpu(), *got[-64 + i][1])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("a", [1.0, 2.0 ** -20, 2.0 ** -59, 2.0 ** -80, 3.40625, 1.2345678, 2.0 ** 60])
+def test_elements_far_above_a_given_maximum(a, dtype, cuda_device):
+    """Codes saturate with their own sign, up to the type's largest numbers; ordinary
+    elements of the same blocks keep their correctly rounded codes."""
+    x = make(dtype, 12, 64, seed=6, std=a)
+    x[0], x[1], x[2, ::2], x[2, 1::2] = 2e38, -2e38, 3e38, -3e38
+    x[3, 5], x[4, 20], x[5, 40], x[6, 63] = 2e38, -2e38, -a * 2.0 ** 60, a * 2.0 ** 66
+    x[7, :16], x[8, :16], x[9, 3] = 20 * a, -20 * a, -7 * a
+    x[10, ::3] = -1e38
+    given = torch.tensor([a], device=cuda_device)
+    data, scale, _ = pkg.situ_glu_nvfp4_quantize(x.to(cuda_device), amax=given)
+    check_codes(x, data, scale, given.cpu(), f"amax {a}")
