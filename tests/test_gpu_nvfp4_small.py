@@ -50,3 +50,23 @@ def test_elements_far_above_a_given_maximum(a, dtype, cuda_device):
     given = torch.tensor([a], device=cuda_device)
     data, scale, _ = pkg.situ_glu_nvfp4_quantize(x.to(cuda_device), amax=given)
     check_codes(x, data, scale, given.cpu(), f"amax {a}")
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_product_offsets_past_32_bits(dtype, cuda_device):
+    """Outputs whose rows, in all, pass 2^32 bytes and elements, and operands with rows far apart."""
+    from test_gpu_nvfp4_product import product_case
+
+    tokens, k, n = 300, 256, 264
+    a, w = product_case(tokens, k, n, [0, 130, tokens], seed=60, device=cuda_device)
+    off = torch.tensor([0, 130, tokens], device=cuda_device)
+    want = pkg.situ_glu_nvfp4_gemm(a, w, off, out_dtype=dtype)
+    pitch = 2 ** 32 // (tokens - 20) // 16 * 16  # elements: the last rows start behind the 2^32nd
+    flat = torch.empty((tokens - 1) * pitch + n, dtype=dtype, device=cuda_device)
+    out = flat.as_strided((tokens, n), (pitch, 1))
+    far = []
+    for t, cols in ((a[0], k // 2), (a[1].view(torch.uint8), k // 16)):  # the rows of codes and of scales, too
+        wide = torch.empty((tokens - 1) * pitch + cols, dtype=torch.uint8, device=cuda_device).as_strided((tokens, cols), (pitch, 1))
+        far.append(wide.copy_(t))
+    got = pkg.situ_glu_nvfp4_gemm((far[0], far[1], a[2]), w, off, out_dtype=dtype, out=out)
+    assert torch.equal(got, want)
