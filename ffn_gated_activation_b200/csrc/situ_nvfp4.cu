@@ -544,6 +544,19 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
+// The factor A_a A_w / 2688^2 as unit * lift.  Sums of products are 0 or lie in [2^-20,
+// 2^54]; where the factor alone leaves the range in which fp32 keeps its precision,
+// they are multiplied by a power of two first, which is exact.
+__device__ __forceinline__ bool unit_in_range(double u) { return fabs(u) >= 0x1p-90 && fabs(u) <= 0x1p90; }
+struct FarUnit {
+  float unit, lift;
+  __device__ __forceinline__ explicit FarUnit(double u) {
+    lift = fabs(u) < 0x1p-90 ? 0x1p-100f : 0x1p64f;
+    const double rest = u / static_cast<double>(lift);
+    unit = fabs(rest) > 3.4e38 ? copysignf(3.402823466e38f, static_cast<float>(rest)) : static_cast<float>(rest);  // 0 stays 0
+  }
+  __device__ __forceinline__ float operator()(uint32_t sum) const { return __uint_as_float(sum) * lift * unit; }
+};
 // Stores 128 bytes of each of a warp's 32 output rows, row0 + lane's in q:
 // columns [c, c + 8 per_vec) of the tile, `per_vec` of them in 16 bytes, those
 // below `cols` (a multiple of 8) and rows below the expert's end.  Through the
@@ -783,13 +796,43 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t empty_addr = peer_addr(&acc_empty[b], 0);
       const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(b * BN);
       const Tile tile = decode_tile<kBM>(t, first_tile, lo, hi, a.experts, n_tiles, BN);
-      const float unit =
-          static_cast<float>(unit_a * (static_cast<double>(a.w_amax[tile.expert * a.w_amax_stride]) / 2688.0));
+      const double factor = unit_a * (static_cast<double>(a.w_amax[tile.expert * a.w_amax_stride]) / 2688.0);
+      const float unit = static_cast<float>(factor);
+      const bool far = !unit_in_range(factor);
       const int64_t row0 = tile.m0 + 128 * rank + quarter * 32;
       const int cols = min(BN, a.n - tile.n0);
       if (!wait_or_abort(&acc_full[b], acc_phase, abort_flag)) break;
       tc_fence_after();
       if (row0 >= tile.m_end) {  // none of the warp's rows exists
+        tc_fence_before();
+        mbar_arrive_remote_relaxed(empty_addr);
+      } else if (far) {  // 128 bytes of the rows at a time; the factor worked out again takes no register till here
+        const FarUnit scale(unit_a * (static_cast<double>(a.w_amax[tile.expert * a.w_amax_stride]) / 2688.0));
+        const int per_vec = a.out_bf16 ? 8 : 4;
+#pragma unroll 1
+        for (int c = 0; c < cols; c += 8 * per_vec) {
+          uint32_t q[32];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t r[16];
+            if (a.out_bf16) {
+              tmem_ld16(taddr + c + 32 * h, r);
+              tmem_ld_wait(r);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) q[16 * h + i] = Bf16::pack(make_float2(scale(r[2 * i]), scale(r[2 * i + 1])));
+              tmem_ld16(taddr + c + 32 * h + 16, r);
+              tmem_ld_wait(r);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) q[16 * h + 8 + i] = Bf16::pack(make_float2(scale(r[2 * i]), scale(r[2 * i + 1])));
+            } else {
+              tmem_ld16(taddr + c + 16 * h, r);
+              tmem_ld_wait(r);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) q[16 * h + i] = __float_as_uint(scale(r[i]));
+            }
+          }
+          put_piece(piece, a, tile, row0, q, c, cols, per_vec);
+        }
         tc_fence_before();
         mbar_arrive_remote_relaxed(empty_addr);
       } else if (a.out_bf16) {

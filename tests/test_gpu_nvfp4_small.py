@@ -70,3 +70,32 @@ def test_product_offsets_past_32_bits(dtype, cuda_device):
         far.append(wide.copy_(t))
     got = pkg.situ_glu_nvfp4_gemm((far[0], far[1], a[2]), w, off, out_dtype=dtype, out=out)
     assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("tokens,n", [(40, 72), (2500, 1544)])  # narrow and wide tiles
+@pytest.mark.parametrize("aa,aw,codes", [(1e-17, 1e-17, None), (1e-20, 1e-16, None), (1e-12, 1e-30, 0x7E), (1e23, 1e23, 0x01),
+                                         (3e38, 1e2, 0x20), (1e-38, 1e38, None), (3e38, 3e38, None), (0.0, 1.0, None)])
+def test_products_of_extreme_tensor_scales(aa, aw, codes, tokens, n, dtype, cuda_device):
+    """The tensor scales' product may leave fp32 where the result does not.  Bound as in
+    test_gpu_nvfp4_product.py, and half of the smallest number of the type."""
+    from test_gpu_nvfp4_product import HALF, U, product_case, values
+
+    k = 128
+    a, w = product_case(tokens, k, n, [0, tokens], seed=61, device=cuda_device)
+    if codes is not None:  # every block scale the same: the smallest, the largest, an ordinary one
+        a[1].view(torch.uint8).fill_(codes)
+        w[1].view(torch.uint8).fill_(codes)
+    a[0][3] = 0
+    a, w = (a[0], a[1], torch.full_like(a[2], aa)), (w[0], w[1], torch.full_like(w[2], aw))
+    got = pkg.situ_glu_nvfp4_gemm(a, w, torch.tensor([0, tokens], device=cuda_device), out_dtype=dtype).cpu().double()
+    av, wv = values(*a), values(w[0][0], w[1][0], w[2])
+    ref, mag = av @ wv.T, av.abs() @ wv.abs().T
+    most = float(torch.finfo(dtype).max)
+    smallest = 2.0 ** -134 if dtype == torch.bfloat16 else 2.0 ** -150
+    bound = (HALF[dtype] + 2 * U) * ref.abs() + 2.0 ** -18 * mag + smallest
+    assert bool((got[3] == 0).all())
+    fine = ref.abs() + bound < most
+    assert bool(((got - ref).abs() <= bound)[fine].all())
+    over = ref.abs() - bound > most  # beyond the type's largest number, whatever the sum's rounding
+    assert bool(((got.abs() >= most) & (torch.sign(got) == torch.sign(ref)))[over].all())
