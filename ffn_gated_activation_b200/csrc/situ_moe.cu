@@ -59,7 +59,7 @@ constexpr int kMoeTileBytes = kMoeRows * kMoeChunk * 2;           // one chunk's
 constexpr int kMoeWeightBytes = kMoeChunks * kMoeTileBytes;       // of a stage
 constexpr int kMoeTile = 16;                         // entries of one box of kernel 2 (32 columns)
 constexpr int kMoeMaxStages = 8;
-constexpr int kMoeTmemCols = 256;                    // two accumulators of 128
+constexpr int kMoeTmemCols = 512;                    // two sets of accumulators, 256 columns each
 constexpr int kMoeSmem = 227 * 1024;
 
 struct MoeArgs {
@@ -213,6 +213,35 @@ __device__ __forceinline__ void moe_mma(uint32_t d, uint64_t a, uint64_t b, uint
 }
 __device__ __forceinline__ uint32_t moe_idesc(int n) {
   return (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n >> 3) << 17) | (8u << 24);
+}
+
+// A unit's k is spread over accumulators of a set, stage by stage: the tensor cores cut
+// off what does not fit into an fp32 accumulator instead of rounding it, so that every
+// addition takes a little of the sum away (activations of 7168 x 2048 in the 2-norm:
+// 1.23e-5 off with one accumulator of 448 additions, 2.7e-6 with eight).  One
+// accumulator for each eight stages of 64 additions, as far as the set's columns go
+// (more would cost: 3 tokens of 1024 x 512 16.5 us with one each way, 16.9 with
+// eight).  Columns from one accumulator to the next:
+constexpr int kMoeSet = kMoeTmemCols / 2;
+__device__ __forceinline__ int moe_apart(int columns, int steps) {
+  const int room = columns <= 32 ? 32 : columns <= 64 ? 64 : 128;
+  const int wish = steps <= 8 ? kMoeSet : steps <= 16 ? kMoeSet / 2 : steps <= 32 ? kMoeSet / 4 : kMoeSet / 8;
+  return max(room, wish);
+}
+// 16 columns of the sum of the accumulators that a unit of `steps` stages has used.
+__device__ __forceinline__ void moe_load16(uint32_t taddr, int apart, int steps, float (&sum)[16]) {
+  uint32_t r[16];
+  fc1::tmem_ld16(taddr, r);
+  fc1::tmem_ld_wait(r);
+#pragma unroll
+  for (int j = 0; j < 16; ++j) sum[j] = __uint_as_float(r[j]);
+#pragma unroll 1
+  for (int at = apart; at < min(kMoeSet, steps * apart); at += apart) {
+    fc1::tmem_ld16(taddr + at, r);
+    fc1::tmem_ld_wait(r);
+#pragma unroll
+    for (int j = 0; j < 16; ++j) sum[j] += __uint_as_float(r[j]);
+  }
 }
 
 // First unit of CTA i of `grid` when `units` are shared out in runs.
@@ -443,16 +472,20 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
         break;
       }
       fc1::tc_fence_after();
-      const uint32_t d = tmem + static_cast<uint32_t>(b * (kMoeTmemCols / 2));
+      const uint32_t d0 = tmem + static_cast<uint32_t>(b * kMoeSet);
       const int n_cols = FC2 ? unit(u).tiles * 2 * kMoeTile : moe_columns(a.tokens, false);
       const uint32_t idesc = moe_idesc(n_cols);
       const uint64_t t_chunk = n_cols * (kMoeChunk * 2 / 16);
+      const int apart = moe_apart(n_cols, steps);
+      int at_col = 0;            // of the stage's accumulator in the set
+      uint32_t accumulate = 0;   // once every accumulator has had a stage
       for (int step = 0; step < steps; ++step) {
         if (!fc1::wait_or_abort(&m.full[stage], phase, m.abort_flag)) {
           ok = false;
           break;
         }
         fc1::tc_fence_after();
+        const uint32_t d = d0 + static_cast<uint32_t>(at_col);
         const uint32_t at = m.ring + stage * stage_bytes;
         const uint64_t w = fc1::smem_desc_sw128(at);
         const uint64_t t = fc1::smem_desc_sw128(at + kMoeWeightBytes);
@@ -461,7 +494,11 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
 #pragma unroll
           for (int s = 0; s < 4; ++s)
             moe_mma(d, w + (c * kMoeTileBytes + s * 32) / 16, t + c * t_chunk + s * 2, idesc,
-                    (step | c | s) != 0 ? 1u : 0u, lane == 0);
+                    (c | s) != 0 ? 1u : accumulate, lane == 0);
+        if ((at_col += apart) == kMoeSet) {
+          at_col = 0;
+          accumulate = 1;
+        }
         if (lane == 0) fc1::umma_commit(&m.empty[stage]);
         __syncwarp();
         if (++stage == stages) {
@@ -494,19 +531,19 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
       if (ok && !fc1::wait_or_abort(&m.acc_full[b], (acc_phase >> b) & 1u, m.abort_flag)) ok = false;
       __syncwarp();
       fc1::tc_fence_after();
-      const uint32_t taddr = lanes + static_cast<uint32_t>(b * (kMoeTmemCols / 2));
+      const uint32_t taddr = lanes + static_cast<uint32_t>(b * kMoeSet);
+      const int apart = moe_apart(FC2 ? v.tiles * 2 * kMoeTile : moe_columns(a.tokens, false), steps);
       if constexpr (FC2) {
         float* out = a.part + static_cast<int64_t>(v.start) * a.hidden + v.block * kMoeRows + row;
         const bool in = v.block * kMoeRows + row < a.hidden;
 #pragma unroll 1
         for (int i = 0; i < v.count; i += 8) {  // eight entries, the value's and the remainder's columns
-          uint32_t r[16];
-          fc1::tmem_ld16(taddr + 2 * i, r);
-          fc1::tmem_ld_wait(r);
+          float r[16];
+          moe_load16(taddr + 2 * i, apart, steps, r);
 #pragma unroll
           for (int j = 0; j < 8; ++j)
             if (in && i + j < v.count)
-              out[static_cast<int64_t>(i + j) * a.hidden] = join_split(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
+              out[static_cast<int64_t>(i + j) * a.hidden] = join_split(r[2 * j], r[2 * j + 1]);
           __syncwarp();
         }
       } else {
@@ -518,14 +555,13 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
         for (int t = 0; t < a.tokens; t += 16) {
           const uint32_t some = static_cast<uint32_t>(mask >> t) & 0xffffu;
           if (some == 0) continue;
-          uint32_t r[16];
-          fc1::tmem_ld16(taddr + t, r);
-          fc1::tmem_ld_wait(r);
+          float r[16];
+          moe_load16(taddr + t, apart, steps, r);
           float(&up)[16][64] = m.plan->up[turn & 1];
           ++turn;
           if (q >= 2) {
 #pragma unroll
-            for (int j = 0; j < 16; ++j) up[j][row & 63] = __uint_as_float(r[j]);
+            for (int j = 0; j < 16; ++j) up[j][row & 63] = r[j];
           }
           asm volatile("bar.sync 1, 128;" ::: "memory");
           if (q < 2) {
@@ -536,7 +572,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
               const float2 w = make_float2(two & 1u ? plan.weight[v.start + entry] : 0.0f,
                                            two & 2u ? plan.weight[v.start + entry + (two & 1u)] : 0.0f);
               const float2 y =
-                  fwd_pair_abs<GATE, HAS_LB, F32>({r[j], r[j + 1]}, {__float_as_uint(up[j][row]), __float_as_uint(up[j + 1][row])},
+                  fwd_pair_abs<GATE, HAS_LB, F32>({__float_as_uint(r[j]), __float_as_uint(r[j + 1])}, {__float_as_uint(up[j][row]), __float_as_uint(up[j + 1][row])},
                                                   mul2(w, splat(a.c.bb)), a.c);
               __nv_bfloat16* o = out + static_cast<int64_t>(entry) * 2 * a.inter;
               if (two & 1u) put_split(o, a.inter, y.x);

@@ -86,3 +86,15 @@ def test_infinite_w1(cuda_device):
     mag = torch.stack([s["w2"][0].double().abs() @ activations(s, 0, t).abs() for t in range(3)])
     # the file's bound of the activations (1e-5 + 2^-17 + 2^-18) and of G and U (2^-18 of ten times their size)
     assert bool(((got[:3].double() - ref).abs() <= 2.0 ** -8 * ref.abs() + 1e-4 * mag).all())
+
+
+def test_long_sums_are_not_cut_off(cuda_device):
+    """7168 terms a sum.  An error of d, relative to y, moves a share of about 0.8 d 2^8 3 of the outputs
+    over a border of bf16 (0.8: the mean of a normal error's size; 3: outputs near zero have narrower
+    steps).  The activations' 16 bits and the arithmetic's 1e-6 are an rms of 3e-6, a share of 0.2 %;
+    448 additions that cut off instead of rounding would be 1.2e-5, 0.7 %.  The border between: 0.4 %."""
+    s = make(4, 7168, 256, 2, 1, seed=44)
+    got = run(s, cuda_device).cpu()
+    ref = torch.stack([s["w2"][e].double() @ activations(s, e, t) for t, e in enumerate(s["ids"][:, 0].tolist())])
+    assert float((got != ref.to(torch.bfloat16)).float().mean()) <= 0.004
+    assert bool(((got.double() - ref).abs() <= 2.0 ** -8 * ref.abs() + 2e-5 * ref.abs().mean()).all())
