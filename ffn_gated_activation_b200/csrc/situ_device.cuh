@@ -771,14 +771,6 @@ __device__ __forceinline__ uint32_t peer_addr(const void* p, uint32_t rank) {
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// The two halves of a barrier that tells only that every CTA of the cluster has
-// started: before it, the shared memory of another one may not be there yet.
-__device__ __forceinline__ void cluster_started() {
-  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void cluster_wait_started() {
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
 __device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* b, uint32_t parity) {
   uint32_t ok;
   asm volatile(

@@ -325,9 +325,14 @@ __global__ void __launch_bounds__(kStoreThreads) situ_nvfp4_quantize_kernel(cons
   else quantize_blocks<S, false, GIVEN>(a, t, first, step);
 }
 
+// The two halves of a barrier that tells only that every CTA of the cluster has
+// started: before it, the shared memory of another one may not be there yet.
+__device__ __forceinline__ void cluster_started() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait_started() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
 // A small matrix in one launch: a cluster of eight CTAs finds A, exchanges it
 // through shared memory and quantises what it has just read (from L2).  Against a
-// fill and two launches (bf16, us in a graph): 7168 blocks 3.6, 6.2; 16576 5.6, 6.2;
+// fill and two launches (bf16, us in a graph): 7168 blocks 3.9, 6.2; 16576 5.7, 6.2;
 // 33152 8.3, 6.2.  Call by call, where the host is the bound, 13.3 and 17.0 up to
 // 49280 blocks; the limit lies between the two.
 constexpr int kSmallCtas = 8, kSmallThreads = 1024;
