@@ -209,7 +209,7 @@ def situ_glu_rms_norm_bwd(grad_y: torch.Tensor, h: torch.Tensor, weight: torch.T
     """Gradients of the forward from its h (x where there was no residual):
     returns (d_x, d_weight or None).  d_x is the gradient of x and of the
     residual; ``grad_h`` is the gradient that reaches h by itself (the residual
-    stream's).  d_weight is summed in fp32 in an order that the shape fixes.
+    stream's).  d_weight is summed in an order that the shape fixes.
     Calls that overlap on the GPU need a ``workspace`` each
     (situ_glu_rms_norm_bwd_workspace_bytes; allocated when not given)."""
     args = _norm_args(h, weight, eps, None)
@@ -325,6 +325,8 @@ def add_rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = DEFAULT_EPS
                  residual: torch.Tensor | None = None):
     """Differentiable residual addition + RMS norm over the last axis: y, or
     (y, h) with a residual (h = x + residual, the residual stream from here on).
+    Gradients whose rows do not start on 16 bytes are copied; a second derivative
+    is an error.
     As with any PyTorch function, a step captured into a CUDA graph whose
     backward() accumulates into leaves' .grad must not share these leaves with an
     eager graph that is still alive: drop that one first, or use
@@ -342,8 +344,11 @@ def situ_glu_moe_fwd(x: torch.Tensor, topk_ids: torch.Tensor, topk_weights: torc
     64 tokens.  x: bf16 [T, H]; topk_ids: int64 [T, k], an id outside
     [0, E) is skipped (-1: an empty slot); topk_weights: [T, k] or None (1);
     w1: bf16 [E, 2I, H] (I gate rows, then I up rows); w2: bf16 [E, H, I].
-    Returns bf16 [T, H].  Calls that overlap on the GPU need a ``workspace``
-    each (situ_glu_moe_workspace_bytes; allocated when not given)."""
+    Returns bf16 [T, H].  w1 and w2 are read where they lie if their last axis is
+    contiguous and the others step as one (a padded row pitch will do); anything
+    else, a transposed weight say, is copied whole in every call: lay it out once.
+    Calls that overlap on the GPU need a ``workspace`` each
+    (situ_glu_moe_workspace_bytes; allocated when not given)."""
     _check_beta(beta, linear_beta)
     device = _cuda(x, "x")
     if not (x.dtype is w1.dtype is w2.dtype is torch.bfloat16):

@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(kNormThreads<V, MX>) situ_rms_norm_fwd_kernel(
 
 // Chunks by the row's width: enough for the CTAs (or, in narrow rows, the warps)
 // that share an SM, few enough that the partial rows stay a few per cent of the
-// traffic (bf16 3000 x 16384: 117 us with 148 chunks, 124 with twice as many).
+// traffic (bf16 3000 x 16384: 136 us with 148 chunks, 141 with twice as many; 2000 x 7168: 25, 27).
 constexpr int kNormMaxChunks = 2368;
 int64_t norm_chunks(int64_t tokens, int64_t hidden) {
   const int64_t most = hidden <= 1024 ? kNormMaxChunks : hidden <= 4096 ? 592 : 148;
@@ -301,8 +301,8 @@ __global__ void __launch_bounds__(kNormThreads<V>) situ_rms_norm_bwd_kernel(cons
     else return dw_reg[i][p];
   };
   // The next row's vectors are loaded while this one is summed, up to two vectors a
-  // thread (bf16 60000 x 256: 26 us, without 32; 40000 x 512: 28, 33); three or four
-  // take the registers of other warps (40000 x 768: 51, without 45).
+  // thread (bf16 60000 x 256: 27 us, without 34; 40000 x 512: 29, 35); three or four
+  // take the registers of other warps (40000 x 768: 52, without 47; 65536 x 1024: 101, 92).
   constexpr bool kAhead = V <= 2;
   auto load = [&](int64_t row, auto& h, auto& g, auto& gh) {
 #pragma unroll
@@ -399,8 +399,11 @@ __global__ void __launch_bounds__(kNormThreads<V>) situ_rms_norm_bwd_kernel(cons
 // The same with the rows staged by bulk copies: warp `warps` of the CTA keeps a
 // ring of whole rows (h, grad_y, grad_h) filled, so the next rows' bytes are in
 // flight while this one is summed; without it a CTA's loads wait for its sums
-// (bf16 16384 x 7168: 259 us; staged 146 us, 6.4 TB/s).  V vectors a thread,
-// the thread's weights and its columns' sums in registers.
+// (bf16 16384 x 7168: 286 us; staged 150 us, 6.3 TB/s).  V vectors a
+// thread, the thread's weights and its columns' sums in registers; with four (rows of
+// more than 1024 vectors) the sums leave no room, some of them spill, and the weights,
+// which are larger than the L1 that the ring leaves, come from L2 twice a row: 3000 x
+// 16384 takes 136 us, more than twice what HBM needs.
 struct NormRing {
   int stages;
   int stage_bytes;
@@ -460,7 +463,7 @@ __global__ void __launch_bounds__(kRingThreads<V>, kRingCtas<S, V, GH>) situ_rms
     return;
   }
   // ---- sums and outputs ----
-  // (four vectors a thread leave no registers for the weights: read from L1 twice a row)
+  // (four vectors a thread leave no registers for the weights: read twice a row)
   constexpr bool kKeep = V < 4;
   float2 kept[kKeep ? V : 1][S::kPairs], dw[V][S::kPairs];
   if constexpr (kKeep) {
@@ -925,8 +928,9 @@ situ_status_t situ_glu_rms_norm_bwd(const void* grad_y, int64_t grad_y_row_strid
   const bool bf = dtype == SITU_DTYPE_BF16;
   // Staged rows from 129 vectors up to 2048, of which two or more fit in shared
   // memory.  Narrower rows have a warp each and enough of them in flight (bf16 65536 x
-  // 1024: 92 us, staged 96; 40000 x 512: 33, staged 48); wider ones gain from the ring
-  // (32768 x 2048: 97 us, direct 105; 8191 x 4096: 51, direct 60).
+  // 1024: 92 us, staged 100; 40000 x 512: 29, staged 51); of the wider ones nearly all
+  // gain from the ring (16384 x 7168: 150 us, direct 286; 8191 x 4096: 48, 52; 32768 x
+  // 1536: 75, 78; 32768 x 2048 with grad_h 98, 92, without 78, 82).
   if (a.vpr > 128 && a.vpr <= 2048) {
     st = launch_norm_ring(a, bf, s);
   } else {

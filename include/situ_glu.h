@@ -415,15 +415,17 @@ situ_status_t situ_attn_res_fwd(const void *blocks, int64_t nblocks, int64_t blo
  *                     NULL: none, and h must be NULL too
  *   weight            [hidden] in weight_dtype, aligned to
  *                     min(16, 16 / sizeof(dtype) * sizeof(weight_dtype)) bytes
- *   epsilon           finite and >= 0
+ *   epsilon           finite and >= 0, rounded to fp32
  *   h                 [tokens, >= hidden] in dtype, written
  *   y                 [tokens, >= hidden] in dtype, written
  * Outputs must not overlap an input or each other.  tokens == 0 launches
  * nothing.  hidden * sizeof(dtype) <= 65536 (SITU_ERR_UNSUPPORTED otherwise)
  * and a multiple of 16, matrices 16-byte aligned with row pitches of a multiple
- * of 16 bytes (SITU_ERR_MISALIGNED).  A row holding a NaN or an
- * infinity has NaNs in y; other rows are not affected.  Results do not depend
- * on the launch size. */
+ * of 16 bytes (SITU_ERR_MISALIGNED).  Rows of any magnitude are
+ * normalised, those too whose squares fp32 does not hold.  A row with a NaN is
+ * all NaN in y, one with an infinity has NaN there and 0 elsewhere, and a row of
+ * zeros with epsilon 0 is NaN; other rows are not affected.  Results do not
+ * depend on the launch size. */
 situ_status_t situ_glu_rms_norm_fwd(const void *x, situ_dtype_t dtype, int64_t tokens, int64_t hidden,
                                     int64_t x_row_stride,
                                     const void *residual, int64_t residual_row_stride,
@@ -448,7 +450,9 @@ situ_status_t situ_glu_rms_norm_fwd_mxfp8(const void *x, situ_dtype_t dtype, int
 /* Backward.  With q[t] = 1 / sqrt(mean_i h[t, i]^2 + epsilon), recomputed from h:
  *   d_x[t, i]   = grad_h[t, i] + q g[t, i] - h[t, i] q^3 mean_j g[t, j] h[t, j],   g = grad_y weight
  *   d_weight[i] = sum_t grad_y[t, i] h[t, i] q[t]
- * d_x is the gradient of both x and residual.
+ * d_x is the gradient of both x and residual.  Rows of any magnitude for which q
+ * and sum_j |g h| are fp32 numbers; a row whose q is not one (rms below 2^-128
+ * with epsilon 0) has infinities or NaN in d_x and gives them to d_weight.
  *
  *   grad_y, h         [tokens, >= hidden] in dtype (h: the forward's h, or x
  *                     where there was no residual)
@@ -456,8 +460,9 @@ situ_status_t situ_glu_rms_norm_fwd_mxfp8(const void *x, situ_dtype_t dtype, int
  *                     dtype, or NULL (zero)
  *   d_x               [tokens, >= hidden] in dtype, written
  *   d_weight          [hidden] in weight_dtype, aligned to its element; NULL: not
- *                     wanted.  Summed in fp32 in an order fixed by the shape (zero
- *                     when tokens == 0).
+ *                     wanted.  Summed in fp32 over a chunk's rows and in double over
+ *                     the chunks, in an order fixed by the shape (zero when
+ *                     tokens == 0).
  *   workspace         >= situ_glu_rms_norm_bwd_workspace_bytes() bytes, 16-byte
  *                     aligned; may be NULL when that is 0
  * Other rules as for situ_glu_rms_norm_fwd. */
@@ -484,7 +489,8 @@ size_t situ_glu_rms_norm_bwd_workspace_bytes(int64_t tokens, int64_t hidden, int
  *   y[t]   = sum over the experts e of token t of W2_e a[t, e]
  * Each expert's weights are read once, whatever the number of its tokens.
  * a enters the second product as a pair of bf16 numbers (its rounding and the
- * remainder's), which keeps 16 bits of its significand.
+ * remainder's), which keeps 16 bits of its significand; an infinite or NaN weight
+ * of W2 meets the rounding alone.
  *
  *   x                 bf16 [tokens, >= hidden], row pitch x_row_stride
  *   topk_ids          DEVICE int64 [tokens, >= topk], row pitch topk_ids_row_stride: the
@@ -555,8 +561,8 @@ situ_status_t situ_glu_nvfp4_dequantize(const void *data, int64_t data_row_strid
  * [offsets[e], offsets[e + 1]) of a),
  *   out[r, n] = sum_k a[r, k] w[e N + n, k]
  * over the values a and w stand for (as situ_glu_nvfp4_dequantize; the block
- * scales enter the tensor cores, A_a A_w / 2688^2 the epilogue), fp32 sums, one
- * rounding to out_dtype.
+ * scales enter the tensor cores, A_a A_w / 2688^2 the epilogue, whether fp32 holds
+ * that factor or not), fp32 sums, one rounding to out_dtype.
  *   a_data, a_scale, a_amax   rows [tokens, k] in NVFP4 (situ_glu_nvfp4_quantize or
  *                             situ_glu_fwd_nvfp4); row pitches in bytes; a_amax one
  *                             DEVICE fp32
