@@ -284,11 +284,12 @@ class AddRMSNormFunction(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, grad_y, grad_h=None):
+        saved = ctx.saved_tensors  # once: hooks that recompute them unpack once
         if not torch.is_grad_enabled():
-            return _norm_grads(ctx, grad_y, grad_h)
+            return _norm_grads(ctx, saved, grad_y, grad_h)
         with torch.no_grad():  # create_graph: a second derivative may follow
-            grads = _norm_grads(ctx, grad_y, grad_h)
-        anchor = next(t for t in ctx.saved_tensors if t.requires_grad)
+            grads = _norm_grads(ctx, saved, grad_y, grad_h)
+        anchor = next(t for t in saved if t.requires_grad)
         given = [g for g in grads if g is not None]
         guarded = iter(_OnceDifferentiable.apply(anchor, *given))
         return tuple(g if g is None else next(guarded) for g in grads)
@@ -308,9 +309,9 @@ class _OnceDifferentiable(torch.autograd.Function):
         raise RuntimeError("add_rms_norm is once_differentiable: it has no second derivative")
 
 
-def _norm_grads(ctx, grad_y, grad_h):
+def _norm_grads(ctx, saved, grad_y, grad_h):
     needs_x, want_dw, _, needs_residual = ctx.needs_input_grad
-    h, weight = ctx.saved_tensors
+    h, weight = saved
     if grad_y is None:  # nothing reached y: the stream's gradient passes through
         d_x, d_w = grad_h, torch.zeros_like(weight) if want_dw else None
     else:  # the engine has checked the gradients' shapes, types and devices, not their alignment

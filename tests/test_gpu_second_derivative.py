@@ -53,3 +53,15 @@ def test_graphs_that_are_not_differentiated_again_run(cuda_device):
     assert all(torch.equal(a.grad.detach(), b) for a, b in zip((x, r, w), want))
     for t in (x, r, w):
         t.grad = None
+
+
+def test_under_checkpointing(cuda_device):
+    """Saved tensors that are recomputed, and may be unpacked once, with and without a graph of the backward."""
+    from torch.utils.checkpoint import checkpoint
+
+    tensors = [t.requires_grad_(True) for t in inputs(cuda_device)]
+    step = lambda x, r, w: sum(t.square().sum() for t in pkg.add_rms_norm(x, w, EPS, residual=r))
+    plain = torch.autograd.grad(step(*tensors), tensors)
+    for create in (False, True):
+        got = torch.autograd.grad(checkpoint(step, *tensors, use_reentrant=False), tensors, create_graph=create)
+        assert all(torch.equal(a, b) for a, b in zip(got, plain))
