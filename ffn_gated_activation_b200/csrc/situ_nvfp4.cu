@@ -558,7 +558,8 @@ struct FarUnit {
   __device__ __forceinline__ explicit FarUnit(double u) {
     lift = fabs(u) < 0x1p-90 ? 0x1p-100f : 0x1p64f;
     const double rest = u / static_cast<double>(lift);
-    unit = fabs(rest) > 3.4e38 ? copysignf(3.402823466e38f, static_cast<float>(rest)) : static_cast<float>(rest);  // 0 stays 0
+    unit = static_cast<float>(rest);
+    if (isinf(unit) && !isinf(u)) unit = copysignf(3.402823466e38f, unit);  // sums of 0 stay 0
   }
   __device__ __forceinline__ float operator()(uint32_t sum) const { return __uint_as_float(sum) * lift * unit; }
 };

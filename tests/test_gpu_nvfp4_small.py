@@ -99,3 +99,17 @@ def test_products_of_extreme_tensor_scales(aa, aw, codes, tokens, n, dtype, cuda
     assert bool(((got - ref).abs() <= bound)[fine].all())
     over = ref.abs() - bound > most  # beyond the type's largest number, whatever the sum's rounding
     assert bool(((got.abs() >= most) & (torch.sign(got) == torch.sign(ref)))[over].all())
+
+
+def test_products_of_tensor_scales_that_are_not_finite(cuda_device):
+    """Zero times an infinite or NaN factor is NaN, as the values say."""
+    from test_gpu_nvfp4_product import product_case
+
+    a, w = product_case(40, 128, 72, [0, 40], seed=62, device=cuda_device)
+    a[0][3] = 0
+    for bad in (float("inf"), float("nan")):
+        for dtype in (torch.bfloat16, torch.float32):
+            for x, y in ((bad, 1.0), (1.0, bad)):
+                got = pkg.situ_glu_nvfp4_gemm((a[0], a[1], torch.full_like(a[2], x)), (w[0], w[1], torch.full_like(w[2], y)),
+                                              out_dtype=dtype)
+                assert bool(torch.isnan(got[3]).all()) and not bool(torch.isfinite(got).any())
